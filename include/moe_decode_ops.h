@@ -1,0 +1,238 @@
+/*
+ * moe_decode_ops.h -- C ABI of the operators beside the decode-step MoE layer
+ * on MI355X (gfx950): the block-scaled fp8 product with its activation
+ * quantiser, and attention over an 8-bit paged cache with its append and its
+ * eviction.
+ *
+ * Conventions (with those of moe_decode.h)
+ *   - Device memory is the caller's, on the plan's device (moe_decode_quant:
+ *     the current device).  Tensors are row-major and contiguous unless a
+ *     stride is given; strides count elements between rows (tokens).
+ *   - bf16 = 16-bit brain float, codes = OCP e4m3fn bytes.  A scale byte b
+ *     (e8m0) means 2^(b-127) and multiplies its codes.
+ *   - Scales that this library makes are the least powers of two that hold
+ *     their block: e = min { e >= -127 : amax <= 448 * 2^e }, code =
+ *     RNE(x * 2^-e).  Both steps are exact but for that one rounding.  amax
+ *     runs over the finite values; an infinity or NaN becomes a NaN code.
+ *   - Runs are asynchronous on `stream`, allocate nothing, do not
+ *     synchronise and may be captured into a HIP graph.  Runs on one plan
+ *     share its workspace and must not overlap (two streams, two graphs).
+ *   - Results do not depend on the order in which workgroups run.
+ *   - Every entry point returns 0 or a moe_decode_status code; checks come
+ *     before any launch.
+ */
+#ifndef MOE_DECODE_OPS_H
+#define MOE_DECODE_OPS_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "moe_decode.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ---- activation quantiser ------------------------------------------------- */
+
+/*
+ * codes [M, K], scales [M, K/128] of x [M, K] bf16, one scale per row and 128
+ * columns.  With limit > 0, x is [M, 2K], gate columns then up columns, and
+ * what is quantised is silu(min(g, limit)) * clamp(u, -limit, limit), the
+ * layer's SwiGLU; codes and scales are then those of its values in 64 bits
+ * (a value next to a rounding border is recomputed in 64 bits).  limit = 0:
+ * x as it is.  K a multiple of 128, at most 65536; M at most 2^20; x_stride a
+ * multiple of 8, at least the columns.
+ * Errors: INVALID_ARG (null or misaligned pointer (x: 16 bytes, codes: 8), negative size,
+ * limit negative or NaN, a stride too small or no multiple of 8), UNSUPPORTED (sizes), HIP.
+ */
+int moe_decode_quant(const void* x, int64_t x_stride, int32_t M, int32_t K, float limit,
+                     void* codes, void* scales, void* stream);
+
+/* ---- block-scaled fp8 product ----------------------------------------------- */
+
+typedef enum { MOE_DECODE_OUT_BF16 = 0, MOE_DECODE_OUT_FP32 = 1 } moe_decode_out_fmt;
+
+/*
+ * y[m, n] = sum over k of x[m, k] * w[n, k]: x codes with a scale byte per row
+ * and 128 columns, w codes with a scale per 128x128 block, fp32 accumulation.
+ * Limits: k a multiple of 128, k <= 65536; 1 <= n <= 2^20;
+ * 1 <= max_rows <= 2^20.
+ */
+typedef struct {
+  int32_t n;
+  int32_t k;
+  int32_t max_rows;  /* largest M a run may pass */
+  int32_t scale_fmt; /* moe_decode_scale_fmt of w_scale */
+  int32_t out_fmt;   /* moe_decode_out_fmt */
+} moe_decode_product_desc;
+
+typedef struct {
+  const void* codes;   /* [M, k] */
+  const void* scales;  /* [M, k/128] bytes */
+  const void* w;       /* [n, k] codes */
+  const void* w_scale; /* [ceil(n/128), k/128] fp32 or bytes */
+  void* out;           /* [M, n] bf16 or fp32, rows out_stride elements apart */
+  int64_t out_stride;  /* at least n */
+} moe_decode_product_args;
+
+typedef struct moe_decode_product_plan_s* moe_decode_product_plan_t;
+
+/* Host-only checks.  INVALID_ARG: null, non-positive size, bad enum, M out of
+ * [0, max_rows], codes or w not 16-byte aligned, w_scale or out not aligned
+ * to its element, a stride below n; UNSUPPORTED: outside the limits. */
+int moe_decode_product_desc_check(const moe_decode_product_desc* d);
+int moe_decode_product_args_check(const moe_decode_product_desc* d,
+                                  const moe_decode_product_args* a, int32_t M);
+
+/* Makes the plan on HIP device `device` (gfx950): the workspace for the
+ * partial sums of few-row products.  Errors as moe_decode_plan. */
+int moe_decode_product_plan(const moe_decode_product_desc* d, int device,
+                            moe_decode_product_plan_t* out);
+int moe_decode_product_run(moe_decode_product_plan_t p, const moe_decode_product_args* a,
+                           int32_t M, void* stream);
+/* Waits for the plan's device and frees its workspace.  NULL is a no-op. */
+int moe_decode_product_destroy(moe_decode_product_plan_t p);
+size_t moe_decode_product_workspace_bytes(moe_decode_product_plan_t p);
+
+/* ---- 8-bit paged cache -------------------------------------------------------- */
+
+/* Tokens of a page. */
+#define MOE_DECODE_PAGE_TOKENS 64
+
+/*
+ * pool [pages, 2, kv_heads, 64 * head_dim] codes and pool_scale [pages, 2,
+ * kv_heads] bytes: K (0) and V (1) of a page and kv head, each with one scale.
+ * Inside a page and head, in the order in which the matrix instructions take
+ * their operands:
+ *   K of token t, dimension d:  byte ((d / 16) * 64 + t) * 16 + d % 16
+ *   V of token t, dimension d:  byte ((t % 16 / 4) * head_dim + d) * 16
+ *                                    + t / 16 * 4 + t % 4
+ * Limits: head_dim 64, 128, 192 or 256; heads a multiple of kv_heads, at most
+ * 16 heads per kv head; kv_heads <= 128; max_batch <= 1024; max_pages <= 16384;
+ * max_q <= 256; pages <= 2^24.
+ */
+typedef struct {
+  int32_t heads;      /* query heads */
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t pages;      /* pages of the pool */
+  int32_t max_batch;  /* sequences of a run */
+  int32_t max_pages;  /* pages of a sequence: columns of the page table */
+  int32_t max_q;      /* new tokens of a sequence in one run */
+  int32_t with_mass;  /* whether runs may ask for mass_out (its workspace) */
+} moe_decode_cache_desc;
+
+/*
+ * The cache as a run of B sequences and T token rows sees it.  Sequence b has
+ * its new tokens in rows q_start[b] .. q_start[b+1]-1 of the run's tensors;
+ * they are the last tokens of its seq_lens[b] (new ones included).  Rows from
+ * q_start[B] on belong to no sequence.  A page may be shared by sequences as
+ * long as none appends to it.
+ * A sequence whose numbers do not fit (q_start not ascending within [0, T],
+ * more than max_q new tokens, a length below its new tokens or past max_pages
+ * pages) is left out: nothing is read or written for it.
+ */
+typedef struct {
+  void* pool;
+  void* pool_scale;
+  const int32_t* page_table; /* [B, max_pages] page ids */
+  const int32_t* seq_lens;   /* [B] */
+  const int32_t* q_start;    /* [B+1] */
+} moe_decode_cache;
+
+/* K and V of the new tokens, [T, kv_heads, head_dim] bf16. */
+typedef struct {
+  moe_decode_cache cache;
+  const void* k;
+  const void* v;
+  int64_t k_stride; /* between tokens; a multiple of 8 */
+  int64_t v_stride;
+} moe_decode_append_args;
+
+typedef struct {
+  moe_decode_cache cache;
+  const void* q;       /* [T, heads, head_dim] bf16 */
+  int64_t q_stride;    /* between tokens; a multiple of 8 */
+  void* out;           /* [T, heads, head_dim] bf16 */
+  int64_t out_stride;  /* between tokens; a multiple of 4 */
+  float sm_scale;      /* scores = sm_scale * q . k */
+  const float* mass_in; /* [B, max_pages] or NULL (zeros) */
+  float* mass_out;      /* [B, max_pages] or NULL; may be mass_in */
+} moe_decode_attend_args;
+
+/*
+ * Per sequence: its first `sink` and last `recent` pages stay; of the others
+ * those of the largest mass, up to `keep` pages in all (equal masses: the
+ * lower index stays; a NaN counts as the largest).  Pages keep their order.
+ * Each output may be its input (table, lens, mass).
+ */
+typedef struct {
+  const int32_t* page_table; /* [B, max_pages] */
+  const int32_t* seq_lens;   /* [B] */
+  const float* mass;         /* [B, max_pages] */
+  int32_t* out_table;        /* [B, max_pages]: the kept pages, then -1 */
+  int32_t* out_lens;         /* [B]: 64 less for each page gone */
+  float* out_mass;           /* [B, max_pages]: the kept pages' mass, then 0 */
+  int32_t* freed;            /* [B, max_pages]: the pages gone, then -1 */
+  int32_t* n_freed;          /* [B] */
+  int32_t keep, sink, recent; /* recent >= 1, sink >= 0, keep >= sink + recent */
+} moe_decode_evict_args;
+
+typedef struct moe_decode_cache_plan_s* moe_decode_cache_plan_t;
+
+/* Host-only checks.  INVALID_ARG: null, non-positive size, B or T out of
+ * range (0 <= B <= max_batch, 0 <= T), a misaligned pointer (pool 16 bytes,
+ * q, k, v 16, out 8) or stride, mass_out without with_mass, mass_in without
+ * mass_out, a non-finite sm_scale, out = q, an eviction's counts; UNSUPPORTED:
+ * outside the limits. */
+int moe_decode_cache_desc_check(const moe_decode_cache_desc* d);
+int moe_decode_append_check(const moe_decode_cache_desc* d, const moe_decode_append_args* a,
+                            int32_t B, int32_t T);
+int moe_decode_attend_check(const moe_decode_cache_desc* d, const moe_decode_attend_args* a,
+                            int32_t B, int32_t T);
+int moe_decode_evict_check(const moe_decode_cache_desc* d, const moe_decode_evict_args* a,
+                           int32_t B);
+
+/* Makes the plan on HIP device `device` (gfx950): the workspace of
+ * moe_decode_cache_attend.  Errors as moe_decode_plan. */
+int moe_decode_cache_plan(const moe_decode_cache_desc* d, int device,
+                          moe_decode_cache_plan_t* out);
+int moe_decode_cache_destroy(moe_decode_cache_plan_t p);
+size_t moe_decode_cache_workspace_bytes(moe_decode_cache_plan_t p);
+
+/*
+ * Writes the new tokens into their pages.  A page's scale only grows while it
+ * fills: where the new tokens need a larger one, the page's earlier codes
+ * are rescaled to it (exact except where a code becomes subnormal: rounded
+ * to nearest even); a page whose first token is new takes the scale that its
+ * new tokens need.  Running the same append again changes nothing.  A token
+ * whose page id is outside the pool is not written.
+ */
+int moe_decode_cache_append(moe_decode_cache_plan_t p, const moe_decode_append_args* a,
+                            int32_t B, int32_t T, void* stream);
+
+/*
+ * out[row of new token j, head h] = softmax(sm_scale * q . K^T) V over the
+ * tokens t < seq_lens[b] - q_b + j + 1 of sequence b, K and V of kv head
+ * h / (heads / kv_heads).  A token sees itself: append first.  Values of
+ * tokens that a row does not see (also non-finite ones, also what lies
+ * behind the sequence's last token) do not reach it.  A row that sees a page
+ * id outside the pool is NaN.  Rows of no sequence are left as they were.
+ * mass_out[b, p] = mass_in[b, p] + the probabilities of page p's tokens summed
+ * over the heads and new tokens of b, for the pages that b has (the others
+ * are left as they were).
+ */
+int moe_decode_cache_attend(moe_decode_cache_plan_t p, const moe_decode_attend_args* a,
+                            int32_t B, int32_t T, void* stream);
+
+/* Chooses the pages that each of B sequences keeps (moe_decode_evict_args).
+ * A sequence with a length outside [0, 64 * max_pages] has its rows copied
+ * whole, nothing freed. */
+int moe_decode_cache_evict(moe_decode_cache_plan_t p, const moe_decode_evict_args* a, int32_t B,
+                           void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* MOE_DECODE_OPS_H */

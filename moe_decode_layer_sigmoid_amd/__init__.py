@@ -1,4 +1,6 @@
-"""MI355X (gfx950) decode-step MoE layer with a sigmoid router.
+"""MI355X (gfx950) decode-step MoE layer with a sigmoid router, and the
+operators beside it: the block-scaled fp8 product with its activation
+quantiser, and attention over an 8-bit paged cache with append and eviction.
 
 The layer runs in hand-written HIP kernels behind the C ABI declared in
 include/moe_decode.h (libmoe_decode.so, built in-tree by
@@ -34,4 +36,27 @@ from .binding import (  # noqa: F401
     run_static,
     strerror,
     PROBE_STEP,
+)
+from .ops import (  # noqa: F401
+    AppendArgs,
+    AttendArgs,
+    Cache,
+    CacheDesc,
+    CachePlan,
+    EvictArgs,
+    OUT_BF16,
+    OUT_FP32,
+    PAGE_TOKENS,
+    ProductArgs,
+    ProductDesc,
+    ProductPlan,
+    append_check,
+    attend_check,
+    cache_desc_check,
+    evict_check,
+    make_cache_desc,
+    make_product_desc,
+    product_args_check,
+    product_desc_check,
+    quant,
 )

@@ -84,6 +84,9 @@ def lib():
         for f in ("desc_check", "args_check", "plan", "run", "destroy", "last_routes",
                   "set_expert_events", "path_for", "check_waits", "read_probe", "run_static"):
             getattr(L, "moe_decode_" + f).restype = ctypes.c_int
+        from . import ops
+
+        ops.declare(L)
         _lib = L
     return _lib
 
@@ -92,7 +95,15 @@ EXPORTED = ["moe_decode_desc_check", "moe_decode_args_check", "moe_decode_plan",
             "moe_decode_run", "moe_decode_destroy", "moe_decode_strerror",
             "moe_decode_last_routes", "moe_decode_set_expert_events", "moe_decode_path_for",
             "moe_decode_check_waits", "moe_decode_workspace_bytes", "moe_decode_read_probe",
-            "moe_decode_run_static"]
+            "moe_decode_run_static",
+            # include/moe_decode_ops.h (bound in ops.py)
+            "moe_decode_quant", "moe_decode_product_desc_check", "moe_decode_product_args_check",
+            "moe_decode_product_plan", "moe_decode_product_run", "moe_decode_product_destroy",
+            "moe_decode_product_workspace_bytes", "moe_decode_cache_desc_check",
+            "moe_decode_append_check", "moe_decode_attend_check", "moe_decode_evict_check",
+            "moe_decode_cache_plan", "moe_decode_cache_destroy",
+            "moe_decode_cache_workspace_bytes", "moe_decode_cache_append",
+            "moe_decode_cache_attend", "moe_decode_cache_evict"]
 
 
 def strerror(code: int) -> str:

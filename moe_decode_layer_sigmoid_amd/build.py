@@ -16,7 +16,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_decode.so")
 SOURCES = ["api.hip", "router.hip", "experts_gemv.hip", "experts_mfma.hip", "epilogue.hip",
-           "experts_chain.hip", "probe.hip"]
+           "experts_chain.hip", "probe.hip", "ops/ops_api.hip", "ops/quant.hip", "ops/product.hip",
+           "ops/cache_append.hip", "ops/cache_attend.hip", "ops/cache_evict.hip"]
 # experts_chain.hip is also compiled once per w13 chunk count (the first
 # template argument of its kernels), each into its own object, in parallel.
 CHAIN_NJG = range(1, 9)
@@ -51,10 +52,10 @@ def build(verbose: bool = False) -> str:
 
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
-    inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
+    inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC, "-I", os.path.join(CSRC, "ops")]
     jobs = []
     for src in SOURCES:
-        obj = os.path.join(objdir, src.replace(".hip", ".o"))
+        obj = os.path.join(objdir, src.replace("/", "_").replace(".hip", ".o"))
         jobs.append((obj, [hipcc(), *FLAGS, *inc, "-c", os.path.join(CSRC, src), "-o", obj]))
     for nj in CHAIN_NJG:
         obj = os.path.join(objdir, "experts_chain_njg%d.o" % nj)

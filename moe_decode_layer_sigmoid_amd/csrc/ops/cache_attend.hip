@@ -1,0 +1,283 @@
+// Attention of a step's new tokens over the 8-bit paged cache.
+//
+// The q_b new tokens of a sequence and the G query heads of a kv head are
+// its rows: row r = j G + i is token j, head i of the group.  A wave takes
+// whole pages of 64 tokens and 16 rows:
+//   S^T = K Q^T   v_mfma_f32_16x16x32_bf16, four tiles of 16 tokens: lane
+//                 (g, c) = (l / 16, l % 16) gets S of tokens 16 s + 4 g + i
+//                 (i < 4) and row c
+//   O^T += V^T P^T  v_mfma_f32_16x16x32_f16: lane (g, c)'s 16 probabilities
+//                 are its operand as they are, and V is stored so that a
+//                 lane's 16 bytes are the same tokens of dimension c.
+// Codes become bf16 / f16 exactly; the page's scale multiplies the scores (K)
+// and the page's contribution (V) in fp32.  P goes in as f16: at most 1, off
+// by at most 2^-12 of itself or 2^-25.  The softmax is kept as a running
+// maximum and sum in fp32, in base 2; waves are joined at the end.
+#include "ops_device.h"
+#include "ops_launch.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kRows = 16;
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ bf16x8_t codes_bf16(uint32_t w0, uint32_t w1) {
+  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false);
+  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true);
+  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false);
+  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true);
+  return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+__device__ __forceinline__ f16x8_t codes_f16(uint32_t w0, uint32_t w1) {
+  const f16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, false);
+  const f16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.0f, true);
+  const f16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, false);
+  const f16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.0f, true);
+  return f16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// 0xff in the bytes of w that are NaN codes.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  // (b & 0x7f) + 1 has bit 7 set only for 0x7f
+  const uint32_t m = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  return (m >> 7) * 0xffu;
+}
+
+// Maximum / sum over the four lane groups that share row c.
+__device__ __forceinline__ float groups_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16, kWave));
+  return fmaxf(v, __shfl_xor(v, 32, kWave));
+}
+__device__ __forceinline__ float groups_sum(float v) {
+  v += __shfl_xor(v, 16, kWave);
+  return v + __shfl_xor(v, 32, kWave);
+}
+
+template <int ND, bool MASS>  // head_dim = 64 ND
+__global__ __launch_bounds__(kThreads) void attend_kernel(AttendArgs a) {
+  constexpr int D = 64 * ND;
+  __shared__ float s_o[kWaves][kRows][D + 4];
+  __shared__ float s_m[kWaves][kRows], s_l[kWaves][kRows];
+  const int r0 = blockIdx.x * kRows, h = blockIdx.y, b = blockIdx.z;
+  const Seq sq = seq_of(a.c, b);
+  if (r0 >= sq.q * a.G) return;  // uniform over the workgroup
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const int rows = sq.q * a.G;
+  const int r = min(r0 + c, rows - 1);
+  const int j = r / a.G;
+  const int lim = sq.len - sq.q + j + 1;            // tokens that row c sees
+  const int lim_lo = sq.len - sq.q + r0 / a.G + 1;  // that every row of the tile sees
+  const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.max_pages;
+  const size_t block_bytes = static_cast<size_t>(kPage) * D;
+
+  // Q operands: chunk q covers dimensions 64 (q / 2) + 16 g + 8 (q % 2) .. + 7
+  bf16x8_t qf[2 * ND];
+  {
+    const uint16_t* qp = a.q + static_cast<int64_t>(sq.q0 + j) * a.q_stride +
+                         (static_cast<int64_t>(h) * a.G + r - j * a.G) * D + 16 * g;
+#pragma unroll
+    for (int i = 0; i < 2 * ND; ++i)
+      qf[i] = __builtin_bit_cast(
+          bf16x8_t, *reinterpret_cast<const uint4*>(qp + 64 * (i >> 1) + 8 * (i & 1)));
+  }
+  f32x4_t acc[4 * ND];
+#pragma unroll
+  for (int t = 0; t < 4 * ND; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  float m = neg_inf(), l = 0.f;  // l: this lane's tokens only
+  const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+  // the last row of the tile sees the most
+  const int last = sq.len - sq.q + (min(r0 + kRows, rows) - 1) / a.G + 1;
+  const int np = (last + kPage - 1) / kPage;
+  for (int pi = wave; pi < np; pi += kWaves) {
+    const int id = table[pi];
+    const bool bad = id < 0 || id >= a.c.pages;
+    const int page = bad ? 0 : id;
+    const size_t kb = page_block(a.c, page, 0, h), vb = page_block(a.c, page, 1, h);
+    const uint8_t* kp = a.c.pool + kb * block_bytes + (g * kPage + c) * 16;
+    const uint8_t* vp = a.c.pool + vb * block_bytes + (g * D + c) * 16;
+    const float ks = a.scale_log2 * e8m0_to_f32(a.c.scale[kb]);
+    const float vs = e8m0_to_f32(a.c.scale[vb]);
+    f32x4_t sc[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      sc[s] = zero;
+#pragma unroll
+      for (int i = 0; i < ND; ++i) {
+        const uint4 w = *reinterpret_cast<const uint4*>(kp + (i * 4 * kPage + 16 * s) * 16);
+        sc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(w.x, w.y), qf[2 * i], sc[s],
+                                                        0, 0, 0);
+        sc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(w.z, w.w), qf[2 * i + 1],
+                                                        sc[s], 0, 0, 0);
+      }
+    }
+    const bool edge = pi * kPage + kPage > lim_lo;  // some row does not see all of the page
+    float pm = neg_inf();
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x = sc[s][i] * ks;
+        if (bad) x = __uint_as_float(0x7fc00000u);
+        if (edge && pi * kPage + 16 * s + 4 * g + i >= lim) x = neg_inf();
+        sc[s][i] = x;
+        pm = fmaxf(pm, x);
+      }
+    const float mn = fmaxf(m, groups_max(pm));
+    const float ref = mn == neg_inf() ? 0.f : mn;
+    const float alpha = exp2_(m - ref);
+    float ps = 0.f;
+    f16x8_t pf[2];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float p = exp2_(sc[s][i] - ref);
+        ps += p;
+        pf[s >> 1][4 * (s & 1) + i] = static_cast<_Float16>(p);
+      }
+    l = l * alpha + ps;
+    m = mn;
+    if (MASS) {
+      const float sum = groups_sum(ps);
+      if (g == 0)
+        a.rec[((static_cast<size_t>(b) * a.c.max_pages + pi) * a.c.Hkv + h) * a.max_rows + r0 +
+              c] = ref + __log2f(sum);
+    }
+#pragma unroll
+    for (int t = 0; t < 4 * ND; ++t) {
+      uint4 w = *reinterpret_cast<const uint4*>(vp + t * 256);
+      f32x4_t nan = zero;
+      if (edge) {
+        // a NaN code reaches only the rows that see it: its place is cleared
+        // and counted under the rows' masks
+        uint32_t x[4] = {w.x, w.y, w.z, w.w}, bits = 0;
+        uint32_t nb[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          nb[k] = nan_bytes(x[k]);
+          bits |= nb[k];
+          x[k] &= ~nb[k];
+        }
+        w = make_uint4(x[0], x[1], x[2], x[3]);
+        if (__any(bits != 0)) {
+          f16x8_t seen[2];
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            seen[q >> 3][q & 7] = static_cast<_Float16>(
+                pi * kPage + 16 * (q >> 2) + 4 * g + (q & 3) < lim ? 1.f : 0.f);
+          // 0x38 is the code of 1
+          nan = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+              codes_f16(nb[0] & 0x38383838u, nb[1] & 0x38383838u), seen[0], nan, 0, 0, 0);
+          nan = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+              codes_f16(nb[2] & 0x38383838u, nb[3] & 0x38383838u), seen[1], nan, 0, 0, 0);
+        }
+      }
+      f32x4_t o = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(w.x, w.y), pf[0], zero, 0, 0, 0);
+      o = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(w.z, w.w), pf[1], o, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[t][i] = fmaf(o[i], vs, acc[t][i] * alpha);
+        if (edge && nan[i] > 0.f) acc[t][i] = __uint_as_float(0x7fc00000u);
+      }
+    }
+  }
+  l = groups_sum(l);
+  // join the waves: dimension 16 t + 4 g + i of row c
+#pragma unroll
+  for (int t = 0; t < 4 * ND; ++t)
+    *reinterpret_cast<f32x4_t*>(&s_o[wave][c][16 * t + 4 * g]) = acc[t];
+  if (g == 0) {
+    s_m[wave][c] = m;
+    s_l[wave][c] = l;
+  }
+  __syncthreads();
+  const int row = threadIdx.x >> 4;
+  if (r0 + row >= rows) return;
+  float mx = s_m[0][row];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) mx = fmaxf(mx, s_m[w][row]);
+  float f[kWaves], sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    f[w] = exp2_(s_m[w][row] - mx);
+    sum += s_l[w][row] * f[w];
+  }
+  const float inv = 1.f / sum;
+  const int jr = (r0 + row) / a.G;
+  uint16_t* op = a.out + static_cast<int64_t>(sq.q0 + jr) * a.out_stride +
+                 (static_cast<int64_t>(h) * a.G + r0 + row - jr * a.G) * D;
+  for (int d = 4 * (threadIdx.x & 15); d < D; d += 64) {
+    float o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) o[i] += s_o[w][row][d + i] * f[w];
+      o[i] *= inv;
+    }
+    *reinterpret_cast<uint2*>(op + d) = make_uint2(f32_to_bf16(o[0]) | f32_to_bf16(o[1]) << 16,
+                                                   f32_to_bf16(o[2]) | f32_to_bf16(o[3]) << 16);
+  }
+  if (MASS && (threadIdx.x & 15) == 0)
+    a.lse[(static_cast<size_t>(b) * a.c.Hkv + h) * a.max_rows + r0 + row] = mx + __log2f(sum);
+}
+
+// mass_out of one page per thread: its share of every row, heads then rows in
+// order.
+__global__ __launch_bounds__(kThreads) void mass_kernel(AttendArgs a) {
+  const int b = blockIdx.y, p = blockIdx.x * kThreads + threadIdx.x;
+  const int32_t q0 = a.c.q_start[b], q1 = a.c.q_start[b + 1], len = a.c.lens[b];
+  const Seq sq = seq_of(a.c, b);
+  if (sq.q == 0 && !(q0 >= 0 && q0 == q1 && q1 <= a.c.T && len >= 0 &&
+                     len <= a.c.max_pages * kPage))
+    return;  // a sequence whose numbers do not fit
+  if (p * kPage >= len) return;
+  const size_t at = static_cast<size_t>(b) * a.c.max_pages + p;
+  float sum = 0.f;
+  for (int h = 0; h < a.c.Hkv; ++h) {
+    const float* rec = a.rec + (at * a.c.Hkv + h) * a.max_rows;
+    const float* lse = a.lse + (static_cast<size_t>(b) * a.c.Hkv + h) * a.max_rows;
+    for (int r = 0; r < sq.q * a.G; ++r) {
+      // rows of a tile whose last token lies before the page have no record
+      const int tile_end = min((r / kRows + 1) * kRows, sq.q * a.G) - 1;
+      if (p * kPage >= sq.len - sq.q + tile_end / a.G + 1) continue;
+      sum += exp2_(rec[r] - lse[r]);
+    }
+  }
+  a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.f) + sum;
+}
+
+template <int ND>
+hipError_t launch(const AttendArgs& a, hipStream_t s) {
+  const dim3 grid(a.max_rows / kRows, a.c.Hkv, a.c.B);
+  if (a.mass_out) hipLaunchKernelGGL((attend_kernel<ND, true>), grid, dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((attend_kernel<ND, false>), grid, dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attend(const AttendArgs& a, hipStream_t s) {
+  const hipError_t e = a.c.D == 64    ? launch<1>(a, s)
+                       : a.c.D == 128 ? launch<2>(a, s)
+                       : a.c.D == 192 ? launch<3>(a, s)
+                                      : launch<4>(a, s);
+  if (e != hipSuccess || !a.mass_out) return e;
+  hipLaunchKernelGGL(mass_kernel, dim3((a.c.max_pages + kThreads - 1) / kThreads, a.c.B),
+                     dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace moe
