@@ -13,6 +13,8 @@
 // and the page's contribution (V) in fp32.  P goes in as f16: at most 1, off
 // by at most 2^-12 of itself or 2^-25.  The softmax is kept as a running
 // maximum and sum in fp32, in base 2; waves are joined at the end.
+#include <algorithm>
+
 #include "ops_device.h"
 #include "ops_launch.h"
 
@@ -22,6 +24,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kRows = 16;
+constexpr int kXcds = 8;
+constexpr int kWantGroups = 2 * 256;
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
@@ -64,174 +68,338 @@ __device__ __forceinline__ float groups_sum(float v) {
   return v + __shfl_xor(v, 32, kWave);
 }
 
+// Least pages of a worker's share: one for each wave.
+constexpr int kMinChunk = kWaves;
+// Partial results whose weights are held in LDS at once while they are joined.
+constexpr int kJoin = 128;
+
+// Exclusive prefix over the sequences of the pages that row tile `rt` reads,
+// in pref[0 .. B] (LDS).  Every thread calls it.
+__device__ __forceinline__ void page_prefix(const AttendArgs& a, int rt, int* pref, int* tmp) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int carry = 0;
+  for (int b0 = 0; b0 < a.c.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    int n = 0;
+    if (b < a.c.B) {
+      const Seq sq = seq_of(a.c, b);
+      if (rt * kRows < sq.q * a.G) n = (sq.len + kPage - 1) / kPage;
+    }
+    int x = n;
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+      const int y = __shfl_up(x, off, kWave);
+      if (lane >= off) x += y;
+    }
+    if (lane == 63) tmp[wave] = x;
+    __syncthreads();
+    int before = carry, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      before += w < wave ? tmp[w] : 0;
+      all += tmp[w];
+    }
+    if (b < a.c.B) pref[b + 1] = before + x;
+    carry += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) pref[0] = 0;
+  __syncthreads();
+}
+
+// Writes dimensions 4 q + 64 i .. + 3 of an output row, o scaled by inv.
+template <int ND>
+__device__ __forceinline__ void store_row(uint16_t* op, int q, const f32x4_t (&o)[ND], float inv) {
+#pragma unroll
+  for (int i = 0; i < ND; ++i)
+    *reinterpret_cast<uint2*>(op + 4 * q + 64 * i) =
+        make_uint2(f32_to_bf16(o[i][0] * inv) | f32_to_bf16(o[i][1] * inv) << 16,
+                   f32_to_bf16(o[i][2] * inv) | f32_to_bf16(o[i][3] * inv) << 16);
+}
+
+// Workers: workgroup (w, y) has kv head y % Hkv and row tile y / Hkv and takes
+// the pages [w chunk, (w + 1) chunk) of all sequences' pages laid end to end,
+// so that every worker reads the same amount whatever the lengths are.  A
+// sequence that lies in one worker is finished there; the parts of one that
+// does not go to slots w + b (unique: along the pages either w or b grows)
+// and the last worker to hand in joins them in order.
 template <int ND, bool MASS>  // head_dim = 64 ND
-__global__ __launch_bounds__(kThreads) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
   constexpr int D = 64 * ND;
   __shared__ float s_o[kWaves][kRows][D + 4];
   __shared__ float s_m[kWaves][kRows], s_l[kWaves][kRows];
-  const int r0 = blockIdx.x * kRows, h = blockIdx.y, b = blockIdx.z;
-  const Seq sq = seq_of(a.c, b);
-  if (r0 >= sq.q * a.G) return;  // uniform over the workgroup
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-  const int rows = sq.q * a.G;
-  const int r = min(r0 + c, rows - 1);
-  const int j = r / a.G;
-  const int lim = sq.len - sq.q + j + 1;            // tokens that row c sees
-  const int lim_lo = sq.len - sq.q + r0 / a.G + 1;  // that every row of the tile sees
-  const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.max_pages;
-  const size_t block_bytes = static_cast<size_t>(kPage) * D;
-
-  // Q operands: chunk q covers dimensions 64 (q / 2) + 16 g + 8 (q % 2) .. + 7
-  bf16x8_t qf[2 * ND];
-  {
-    const uint16_t* qp = a.q + static_cast<int64_t>(sq.q0 + j) * a.q_stride +
-                         (static_cast<int64_t>(h) * a.G + r - j * a.G) * D + 16 * g;
-#pragma unroll
-    for (int i = 0; i < 2 * ND; ++i)
-      qf[i] = __builtin_bit_cast(
-          bf16x8_t, *reinterpret_cast<const uint4*>(qp + 64 * (i >> 1) + 8 * (i & 1)));
-  }
-  f32x4_t acc[4 * ND];
-#pragma unroll
-  for (int t = 0; t < 4 * ND; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  float m = neg_inf(), l = 0.f;  // l: this lane's tokens only
-  const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-  // the last row of the tile sees the most
-  const int last = sq.len - sq.q + (min(r0 + kRows, rows) - 1) / a.G + 1;
-  const int np = (last + kPage - 1) / kPage;
-  for (int pi = wave; pi < np; pi += kWaves) {
-    const int id = table[pi];
-    const bool bad = id < 0 || id >= a.c.pages;
-    const int page = bad ? 0 : id;
-    const size_t kb = page_block(a.c, page, 0, h), vb = page_block(a.c, page, 1, h);
-    const uint8_t* kp = a.c.pool + kb * block_bytes + (g * kPage + c) * 16;
-    const uint8_t* vp = a.c.pool + vb * block_bytes + (g * D + c) * 16;
-    const float ks = a.scale_log2 * e8m0_to_f32(a.c.scale[kb]);
-    const float vs = e8m0_to_f32(a.c.scale[vb]);
-    f32x4_t sc[4];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      sc[s] = zero;
-#pragma unroll
-      for (int i = 0; i < ND; ++i) {
-        const uint4 w = *reinterpret_cast<const uint4*>(kp + (i * 4 * kPage + 16 * s) * 16);
-        sc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(w.x, w.y), qf[2 * i], sc[s],
-                                                        0, 0, 0);
-        sc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(w.z, w.w), qf[2 * i + 1],
-                                                        sc[s], 0, 0, 0);
-      }
-    }
-    const bool edge = pi * kPage + kPage > lim_lo;  // some row does not see all of the page
-    float pm = neg_inf();
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float x = sc[s][i] * ks;
-        if (bad) x = __uint_as_float(0x7fc00000u);
-        if (edge && pi * kPage + 16 * s + 4 * g + i >= lim) x = neg_inf();
-        sc[s][i] = x;
-        pm = fmaxf(pm, x);
-      }
-    const float mn = fmaxf(m, groups_max(pm));
-    const float ref = mn == neg_inf() ? 0.f : mn;
-    const float alpha = exp2_(m - ref);
-    float ps = 0.f;
-    f16x8_t pf[2];
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p = exp2_(sc[s][i] - ref);
-        ps += p;
-        pf[s >> 1][4 * (s & 1) + i] = static_cast<_Float16>(p);
-      }
-    l = l * alpha + ps;
-    m = mn;
-    if (MASS) {
-      const float sum = groups_sum(ps);
-      if (g == 0)
-        a.rec[((static_cast<size_t>(b) * a.c.max_pages + pi) * a.c.Hkv + h) * a.max_rows + r0 +
-              c] = ref + __log2f(sum);
-    }
-#pragma unroll
-    for (int t = 0; t < 4 * ND; ++t) {
-      uint4 w = *reinterpret_cast<const uint4*>(vp + t * 256);
-      f32x4_t nan = zero;
-      if (edge) {
-        // a NaN code reaches only the rows that see it: its place is cleared
-        // and counted under the rows' masks
-        uint32_t x[4] = {w.x, w.y, w.z, w.w}, bits = 0;
-        uint32_t nb[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          nb[k] = nan_bytes(x[k]);
-          bits |= nb[k];
-          x[k] &= ~nb[k];
-        }
-        w = make_uint4(x[0], x[1], x[2], x[3]);
-        if (__any(bits != 0)) {
-          f16x8_t seen[2];
-#pragma unroll
-          for (int q = 0; q < 16; ++q)
-            seen[q >> 3][q & 7] = static_cast<_Float16>(
-                pi * kPage + 16 * (q >> 2) + 4 * g + (q & 3) < lim ? 1.f : 0.f);
-          // 0x38 is the code of 1
-          nan = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-              codes_f16(nb[0] & 0x38383838u, nb[1] & 0x38383838u), seen[0], nan, 0, 0, 0);
-          nan = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-              codes_f16(nb[2] & 0x38383838u, nb[3] & 0x38383838u), seen[1], nan, 0, 0, 0);
-        }
-      }
-      f32x4_t o = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(w.x, w.y), pf[0], zero, 0, 0, 0);
-      o = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(w.z, w.w), pf[1], o, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[t][i] = fmaf(o[i], vs, acc[t][i] * alpha);
-        if (edge && nan[i] > 0.f) acc[t][i] = __uint_as_float(0x7fc00000u);
-      }
-    }
-  }
-  l = groups_sum(l);
-  // join the waves: dimension 16 t + 4 g + i of row c
-#pragma unroll
-  for (int t = 0; t < 4 * ND; ++t)
-    *reinterpret_cast<f32x4_t*>(&s_o[wave][c][16 * t + 4 * g]) = acc[t];
-  if (g == 0) {
-    s_m[wave][c] = m;
-    s_l[wave][c] = l;
-  }
+  __shared__ float s_f[kJoin][kRows];
+  __shared__ int s_pref[kMaxBatch + 1];
+  __shared__ int s_tmp[kWaves];
+  __shared__ int s_b, s_last;
+  const int h = blockIdx.y % a.c.Hkv, rt = blockIdx.y / a.c.Hkv, r0 = rt * kRows;
+  const int tid = threadIdx.x;
+  page_prefix(a, rt, s_pref, s_tmp);
+  const int N = s_pref[a.c.B];
+  const int chunk = max((N + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x),
+                        kMinChunk);
+  const int w_lo = blockIdx.x * chunk, w_hi = min(w_lo + chunk, N);
+  if (w_lo >= w_hi) return;  // uniform over the workgroup
+  for (int b = tid; b < a.c.B; b += kThreads)
+    if (s_pref[b] <= w_lo && w_lo < s_pref[b + 1]) s_b = b;
   __syncthreads();
-  const int row = threadIdx.x >> 4;
-  if (r0 + row >= rows) return;
-  float mx = s_m[0][row];
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = tid & 63, g = lane >> 4, c = lane & 15;
+  const size_t block_bytes = static_cast<size_t>(kPage) * D;
+  const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+
+  for (int at = w_lo, b = s_b; at < w_hi; ++b) {
+    const int first = s_pref[b], n_pages = s_pref[b + 1] - first;
+    if (n_pages == 0) continue;
+    const Seq sq = seq_of(a.c, b);
+    const int rows = sq.q * a.G;
+    const int r = min(r0 + c, rows - 1);
+    const int j = r / a.G;
+    const int lim = sq.len - sq.q + j + 1;            // tokens that row c sees
+    const int lim_lo = sq.len - sq.q + r0 / a.G + 1;  // that every row of the tile sees
+    const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.max_pages;
+    const int p_lo = at - first, p_hi = min(w_hi - first, n_pages);
+
+    // Q operands: chunk q covers dimensions 64 (q / 2) + 16 g + 8 (q % 2) .. + 7
+    bf16x8_t qf[2 * ND];
+    {
+      const uint16_t* qp = a.q + static_cast<int64_t>(sq.q0 + j) * a.q_stride +
+                           (static_cast<int64_t>(h) * a.G + r - j * a.G) * D + 16 * g;
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) mx = fmaxf(mx, s_m[w][row]);
-  float f[kWaves], sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    f[w] = exp2_(s_m[w][row] - mx);
-    sum += s_l[w][row] * f[w];
-  }
-  const float inv = 1.f / sum;
-  const int jr = (r0 + row) / a.G;
-  uint16_t* op = a.out + static_cast<int64_t>(sq.q0 + jr) * a.out_stride +
-                 (static_cast<int64_t>(h) * a.G + r0 + row - jr * a.G) * D;
-  for (int d = 4 * (threadIdx.x & 15); d < D; d += 64) {
-    float o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[i] = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) o[i] += s_o[w][row][d + i] * f[w];
-      o[i] *= inv;
+      for (int i = 0; i < 2 * ND; ++i)
+        qf[i] = __builtin_bit_cast(
+            bf16x8_t, *reinterpret_cast<const uint4*>(qp + 64 * (i >> 1) + 8 * (i & 1)));
     }
-    *reinterpret_cast<uint2*>(op + d) = make_uint2(f32_to_bf16(o[0]) | f32_to_bf16(o[1]) << 16,
-                                                   f32_to_bf16(o[2]) | f32_to_bf16(o[3]) << 16);
+    f32x4_t acc[4 * ND];
+#pragma unroll
+    for (int t = 0; t < 4 * ND; ++t) acc[t] = zero;
+    float m = neg_inf(), l = 0.f;  // l: this lane's tokens only
+
+    // a page's K operands and scales; the next page's are loaded while this
+    // one's scores are turned into probabilities
+    uint4 kw[4 * ND];
+    uint32_t ks8 = 0, vs8 = 0;
+    const uint8_t* vp = a.c.pool;
+    bool bad = false;
+    int ids = 0;
+    auto load_page = [&](int pi) {
+      // lane i holds the id of the wave's i-th page from here on
+      const int i = (pi - p_lo) / kWaves;
+      if ((i & 63) == 0) ids = table[min(pi + kWaves * lane, p_hi - 1)];
+      const int id = __builtin_amdgcn_readlane(ids, i & 63);
+      bad = id < 0 || id >= a.c.pages;
+      const int page = bad ? 0 : id;
+      const size_t kb = page_block(a.c, page, 0, h), vb = page_block(a.c, page, 1, h);
+      const uint8_t* kp = a.c.pool + kb * block_bytes + (g * kPage + c) * 16;
+      vp = a.c.pool + vb * block_bytes + (g * D + c) * 16;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+          kw[s * ND + i] = *reinterpret_cast<const uint4*>(kp + (i * 4 * kPage + 16 * s) * 16);
+      ks8 = a.c.scale[kb];
+      vs8 = a.c.scale[vb];
+    };
+    if (p_lo + wave < p_hi) load_page(p_lo + wave);
+    for (int pi = p_lo + wave; pi < p_hi; pi += kWaves) {
+      uint4 vw[4 * ND];
+#pragma unroll
+      for (int t = 0; t < 4 * ND; ++t) vw[t] = *reinterpret_cast<const uint4*>(vp + t * 256);
+      const float ks = a.scale_log2 * e8m0_to_f32(ks8), vs = e8m0_to_f32(vs8);
+      const bool bad_now = bad;
+      f32x4_t sc[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        sc[s] = zero;
+#pragma unroll
+        for (int i = 0; i < ND; ++i) {
+          const uint4 w = kw[s * ND + i];
+          sc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(w.x, w.y), qf[2 * i], sc[s],
+                                                          0, 0, 0);
+          sc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(w.z, w.w), qf[2 * i + 1],
+                                                          sc[s], 0, 0, 0);
+        }
+      }
+      if (pi + kWaves < p_hi) load_page(pi + kWaves);
+      const bool edge = pi * kPage + kPage > lim_lo;  // some row does not see all of the page
+      float pm = neg_inf();
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x = sc[s][i] * ks;
+          if (bad_now) x = __uint_as_float(0x7fc00000u);
+          if (edge && pi * kPage + 16 * s + 4 * g + i >= lim) x = neg_inf();
+          sc[s][i] = x;
+          pm = fmaxf(pm, x);
+        }
+      const float mn = fmaxf(m, groups_max(pm));
+      const float ref = mn == neg_inf() ? 0.f : mn;
+      const float alpha = exp2_(m - ref);
+      float ps = 0.f;
+      f16x8_t pf[2];
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = exp2_(sc[s][i] - ref);
+          ps += p;
+          pf[s >> 1][4 * (s & 1) + i] = static_cast<_Float16>(p);
+        }
+      l = l * alpha + ps;
+      m = mn;
+      if (MASS) {
+        const float sum = groups_sum(ps);
+        if (g == 0)
+          a.rec[((static_cast<size_t>(b) * a.c.max_pages + pi) * a.c.Hkv + h) * a.max_rows + r0 +
+                c] = ref + __log2f(sum);
+      }
+#pragma unroll
+      for (int t = 0; t < 4 * ND; ++t) {
+        uint4 w = vw[t];
+        f32x4_t nan = zero;
+        if (edge) {
+          // a NaN code reaches only the rows that see it: its place is cleared
+          // and counted under the rows' masks
+          uint32_t x[4] = {w.x, w.y, w.z, w.w}, bits = 0;
+          uint32_t nb[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            nb[k] = nan_bytes(x[k]);
+            bits |= nb[k];
+            x[k] &= ~nb[k];
+          }
+          w = make_uint4(x[0], x[1], x[2], x[3]);
+          if (__any(bits != 0)) {
+            f16x8_t seen[2];
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+              seen[q >> 3][q & 7] = static_cast<_Float16>(
+                  pi * kPage + 16 * (q >> 2) + 4 * g + (q & 3) < lim ? 1.f : 0.f);
+            // 0x38 is the code of 1
+            nan = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                codes_f16(nb[0] & 0x38383838u, nb[1] & 0x38383838u), seen[0], nan, 0, 0, 0);
+            nan = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                codes_f16(nb[2] & 0x38383838u, nb[3] & 0x38383838u), seen[1], nan, 0, 0, 0);
+          }
+        }
+        f32x4_t o =
+            __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(w.x, w.y), pf[0], zero, 0, 0, 0);
+        o = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(w.z, w.w), pf[1], o, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[t][i] = fmaf(o[i], vs, acc[t][i] * alpha);
+          if (edge && nan[i] > 0.f) acc[t][i] = __uint_as_float(0x7fc00000u);
+        }
+      }
+    }
+    l = groups_sum(l);
+    // join the waves: dimension 16 t + 4 g + i of row c
+    __syncthreads();  // the last segment's readers are done
+#pragma unroll
+    for (int t = 0; t < 4 * ND; ++t)
+      *reinterpret_cast<f32x4_t*>(&s_o[wave][c][16 * t + 4 * g]) = acc[t];
+    if (g == 0) {
+      s_m[wave][c] = m;
+      s_l[wave][c] = l;
+    }
+    __syncthreads();
+    const int row = tid >> 4, q = tid & 15, valid = min(kRows, rows - r0);
+    float mx = s_m[0][row];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) mx = fmaxf(mx, s_m[w][row]);
+    const float ref = mx == neg_inf() ? 0.f : mx;  // a part may see no token
+    float f[kWaves], sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      f[w] = exp2_(s_m[w][row] - ref);
+      sum += s_l[w][row] * f[w];
+    }
+    f32x4_t o[ND];
+#pragma unroll
+    for (int i = 0; i < ND; ++i) {
+      o[i] = zero;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w)
+        o[i] += *reinterpret_cast<const f32x4_t*>(&s_o[w][row][4 * q + 64 * i]) * f[w];
+    }
+    const int out_j = (r0 + row) / a.G;
+    uint16_t* op = a.out + static_cast<int64_t>(sq.q0 + out_j) * a.out_stride +
+                   (static_cast<int64_t>(h) * a.G + r0 + row - out_j * a.G) * D;
+    float* lse = a.lse + (static_cast<size_t>(b) * a.c.Hkv + h) * a.max_rows + r0 + row;
+    if (p_hi - p_lo == n_pages) {
+      if (row < valid) {
+        store_row<ND>(op, q, o, 1.f / sum);
+        if (MASS && q == 0) *lse = mx + __log2f(sum);
+      }
+    } else {
+      // hand in: slots w0 + b .. w1 + b are the sequence's parts
+      const int w0 = first / chunk, w1 = (first + n_pages - 1) / chunk, parts = w1 - w0 + 1;
+      const size_t slot0 =
+          static_cast<size_t>(blockIdx.y) * (gridDim.x + a.c.B) + w0 + b;  // part 0
+      const size_t mine = slot0 + (blockIdx.x - w0);
+      float* po = a.part_o + mine * kRows * D;
+      if (row < valid) {
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+          st_f32x4<true>(po + row * D + 4 * q + 64 * i,
+                         make_float4(o[i][0], o[i][1], o[i][2], o[i][3]));
+        if (q == 0) {
+          st_f32<true>(a.part_ml + (mine * kRows + row) * 2, mx);
+          st_f32<true>(a.part_ml + (mine * kRows + row) * 2 + 1, sum);
+        }
+      }
+      wait_memory();
+      __syncthreads();
+      uint32_t* cnt = a.count + static_cast<size_t>(blockIdx.y) * a.c.B + b;
+      if (tid == 0)
+        s_last = __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                 static_cast<uint32_t>(parts) - 1;
+      __syncthreads();
+      if (s_last) {
+        if (tid == 0) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const float* ml = a.part_ml + slot0 * kRows * 2;
+        float top = neg_inf();
+        if (row < valid)
+          for (int p = q; p < parts; p += 16)
+            top = fmaxf(top, ld_f32<true>(ml + (p * kRows + row) * 2));
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
+        float total = 0.f;
+#pragma unroll
+        for (int i = 0; i < ND; ++i) o[i] = zero;
+        for (int p0 = 0; p0 < parts; p0 += kJoin) {
+          const int np = min(kJoin, parts - p0);
+          __syncthreads();
+          if (row < valid)
+            for (int p = q; p < np; p += 16) {
+              const float* x = ml + ((p0 + p) * kRows + row) * 2;
+              const float w = exp2_(ld_f32<true>(x) - top);
+              s_f[p][row] = w;
+              total += ld_f32<true>(x + 1) * w;
+            }
+          __syncthreads();
+          if (row < valid)
+            for (int p = 0; p < np; ++p) {
+              const float w = s_f[p][row];
+              const float* x = a.part_o + ((slot0 + p0 + p) * kRows + row) * D + 4 * q;
+#pragma unroll
+              for (int i = 0; i < ND; ++i) {
+                const float4 y = ld_f32x4<true>(x + 64 * i);
+                o[i] += f32x4_t{y.x, y.y, y.z, y.w} * w;
+              }
+            }
+        }
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) total += __shfl_xor(total, off, kWave);
+        if (row < valid) {
+          store_row<ND>(op, q, o, 1.f / total);
+          if (MASS && q == 0) *lse = top + __log2f(total);
+        }
+      }
+    }
+    at = first + p_hi;
   }
-  if (MASS && (threadIdx.x & 15) == 0)
-    a.lse[(static_cast<size_t>(b) * a.c.Hkv + h) * a.max_rows + r0 + row] = mx + __log2f(sum);
 }
 
 // mass_out of one page per thread: its share of every row, heads then rows in
@@ -249,25 +417,30 @@ __global__ __launch_bounds__(kThreads) void mass_kernel(AttendArgs a) {
   for (int h = 0; h < a.c.Hkv; ++h) {
     const float* rec = a.rec + (at * a.c.Hkv + h) * a.max_rows;
     const float* lse = a.lse + (static_cast<size_t>(b) * a.c.Hkv + h) * a.max_rows;
-    for (int r = 0; r < sq.q * a.G; ++r) {
-      // rows of a tile whose last token lies before the page have no record
-      const int tile_end = min((r / kRows + 1) * kRows, sq.q * a.G) - 1;
-      if (p * kPage >= sq.len - sq.q + tile_end / a.G + 1) continue;
-      sum += exp2_(rec[r] - lse[r]);
-    }
+    for (int r = 0; r < sq.q * a.G; ++r) sum += exp2_(rec[r] - lse[r]);
   }
   a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.f) + sum;
 }
 
 template <int ND>
 hipError_t launch(const AttendArgs& a, hipStream_t s) {
-  const dim3 grid(a.max_rows / kRows, a.c.Hkv, a.c.B);
+  const dim3 grid(a.workers, a.c.Hkv * (a.max_rows / kRows));
   if (a.mass_out) hipLaunchKernelGGL((attend_kernel<ND, true>), grid, dim3(kThreads), 0, s, a);
   else hipLaunchKernelGGL((attend_kernel<ND, false>), grid, dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
 }  // namespace
+
+// Enough workgroups for two per CU, of no fewer than kMinChunk pages each, a
+// multiple of the XCDs (a worker's row tiles then read its pages from one L2).
+int attend_workers(int Hkv, int max_rows, int max_batch, int max_pages) {
+  const int64_t y = static_cast<int64_t>(Hkv) * (max_rows / kRows);
+  const int64_t pages = static_cast<int64_t>(max_batch) * max_pages;
+  int64_t w = (kWantGroups + y - 1) / y;
+  w = std::min(w, (pages + kMinChunk - 1) / kMinChunk);
+  return static_cast<int>((w + kXcds - 1) / kXcds * kXcds);
+}
 
 hipError_t launch_attend(const AttendArgs& a, hipStream_t s) {
   const hipError_t e = a.c.D == 64    ? launch<1>(a, s)

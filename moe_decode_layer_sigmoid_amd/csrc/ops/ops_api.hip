@@ -100,7 +100,17 @@ size_t cache_layout(const moe_decode_cache_desc& d, char* base, moe::AttendArgs*
   const size_t mass = d.with_mass ? 1 : 0;
   char* lse = take(mass * B * heads * rows * 4);
   char* rec = take(mass * B * d.max_pages * heads * rows * 4);
+  const size_t y = heads * (rows / 16);
+  const size_t workers = moe::attend_workers(d.kv_heads, static_cast<int>(rows), d.max_batch,
+                                             d.max_pages);
+  char* part_o = take(y * (workers + B) * 16 * d.head_dim * 4);
+  char* part_ml = take(y * (workers + B) * 16 * 2 * 4);
+  char* count = take(y * B * 4);
   if (a) {
+    a->workers = static_cast<int>(workers);
+    a->part_o = reinterpret_cast<float*>(part_o);
+    a->part_ml = reinterpret_cast<float*>(part_ml);
+    a->count = reinterpret_cast<uint32_t*>(count);
     a->lse = reinterpret_cast<float*>(lse);
     a->rec = reinterpret_cast<float*>(rec);
   }
@@ -250,7 +260,7 @@ int moe_decode_cache_desc_check(const moe_decode_cache_desc* d) {
     return MOE_DECODE_ERR_INVALID_ARG;
   if (d->with_mass != 0 && d->with_mass != 1) return MOE_DECODE_ERR_INVALID_ARG;
   if (d->head_dim % 64 || d->head_dim > 256 || d->heads % d->kv_heads ||
-      d->heads / d->kv_heads > 16 || d->kv_heads > 128 || d->max_batch > 1024 ||
+      d->heads / d->kv_heads > 16 || d->kv_heads > 128 || d->max_batch > moe::kMaxBatch ||
       d->max_pages > 16384 || d->max_q > 256 || d->pages > (1 << 24))
     return MOE_DECODE_ERR_UNSUPPORTED;
   return MOE_DECODE_OK;

@@ -9,6 +9,7 @@
 namespace moe {
 
 constexpr int kPage = MOE_DECODE_PAGE_TOKENS;
+constexpr int kMaxBatch = 1024;
 
 // ---- quantiser ----------------------------------------------------------------
 hipError_t launch_quant(const uint16_t* x, int64_t x_stride, int M, int K, float limit,
@@ -71,7 +72,14 @@ struct AttendArgs {
   float* mass_out;
   float* rec;  // [B][max_pages][Hkv][max_rows]: log2 of a page's share of each row
   float* lse;  // [B][Hkv][max_rows]
+  // workgroups per kv head and row tile, and what they hand to each other
+  int workers;
+  float* part_o;    // [y][workers + B][16][D]
+  float* part_ml;   // [y][workers + B][16][2]: maximum, sum
+  uint32_t* count;  // [y][B] parts handed in; 0 between runs
 };
+// Workgroups per kv head and row tile.
+int attend_workers(int Hkv, int max_rows, int max_batch, int max_pages);
 hipError_t launch_attend(const AttendArgs& a, hipStream_t s);
 
 struct EvictArgs {
