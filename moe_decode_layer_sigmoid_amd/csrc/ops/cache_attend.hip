@@ -24,8 +24,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kRows = 16;
+constexpr int kTeams = kThreads / 16;  // sixteen threads that hold one row
 constexpr int kXcds = 8;
-constexpr int kWantGroups = 2 * 256;
+// Workgroups of a launch: one per CU.  Measured at one sequence of 131000
+// tokens, 8 kv heads of 128: 50.6 us; two per CU 57.5 (the same bytes from
+// twice as many places at once, and twice the parts to join), one of 512
+// threads 52.7.
+constexpr int kWantGroups = 256;
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
@@ -58,6 +63,15 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return (m >> 7) * 0xffu;
 }
 
+typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+
+// Sixteen bytes; NT: not kept in the caches.
+template <bool NT>
+__device__ __forceinline__ uint4 load16(const uint8_t* p) {
+  const u32x4_t* q = reinterpret_cast<const u32x4_t*>(p);
+  return __builtin_bit_cast(uint4, NT ? __builtin_nontemporal_load(q) : *q);
+}
+
 // Maximum / sum over the four lane groups that share row c.
 __device__ __forceinline__ float groups_max(float v) {
   v = fmaxf(v, __shfl_xor(v, 16, kWave));
@@ -70,8 +84,6 @@ __device__ __forceinline__ float groups_sum(float v) {
 
 // Least pages of a worker's share: one for each wave.
 constexpr int kMinChunk = kWaves;
-// Partial results whose weights are held in LDS at once while they are joined.
-constexpr int kJoin = 128;
 
 // Exclusive prefix over the sequences of the pages that row tile `rt` reads,
 // in pref[0 .. B] (LDS).  Every thread calls it.
@@ -123,12 +135,16 @@ __device__ __forceinline__ void store_row(uint16_t* op, int q, const f32x4_t (&o
 // sequence that lies in one worker is finished there; the parts of one that
 // does not go to slots w + b (unique: along the pages either w or b grows)
 // and the last worker to hand in joins them in order.
-template <int ND, bool MASS>  // head_dim = 64 ND
-__global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
+// head_dim = 64 ND; ONCE: one row tile, so that no other workgroup reads the
+// same codes and the loads need not stay in the caches.
+template <int ND, bool MASS, bool ONCE>
+__global__ __launch_bounds__(kThreads, ND <= 2 ? 2 : 1) void attend_kernel(AttendArgs a) {
   constexpr int D = 64 * ND;
-  __shared__ float s_o[kWaves][kRows][D + 4];
+  constexpr int kJoin = ND <= 2 ? 8 : 4;  // parts that a thread loads at once
+  __shared__ __attribute__((aligned(16))) float s_o[kWaves][kRows][D + 4];
+  auto& s_j = *reinterpret_cast<float(*)[kTeams][D + 4]>(s_o);
+  static_assert(kTeams <= kWaves * kRows, "a row of s_o per team");
   __shared__ float s_m[kWaves][kRows], s_l[kWaves][kRows];
-  __shared__ float s_f[kJoin][kRows];
   __shared__ int s_pref[kMaxBatch + 1];
   __shared__ int s_tmp[kWaves];
   __shared__ int s_b, s_last;
@@ -175,121 +191,158 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
     for (int t = 0; t < 4 * ND; ++t) acc[t] = zero;
     float m = neg_inf(), l = 0.f;  // l: this lane's tokens only
 
-    // a page's K operands and scales; the next page's are loaded while this
-    // one's scores are turned into probabilities
-    uint4 kw[4 * ND];
-    uint32_t ks8 = 0, vs8 = 0;
-    const uint8_t* vp = a.c.pool;
-    bool bad = false;
-    int ids = 0;
-    auto load_page = [&](int pi) {
-      // lane i holds the id of the wave's i-th page from here on
-      const int i = (pi - p_lo) / kWaves;
-      if ((i & 63) == 0) ids = table[min(pi + kWaves * lane, p_hi - 1)];
-      const int id = __builtin_amdgcn_readlane(ids, i & 63);
+    // A page's operands and scales.  Each register is loaded with the next
+    // page's bytes as soon as the matrix instruction has taken this page's, so
+    // a whole page per wave is in flight at any time.
+    uint4 kw[4 * ND], vw[4 * ND];
+    uint32_t ks8, vs8;
+    bool bad;
+    size_t kb, vb;
+    const uint8_t *kp, *vp;
+    auto find_page = [&](int id) {
       bad = id < 0 || id >= a.c.pages;
       const int page = bad ? 0 : id;
-      const size_t kb = page_block(a.c, page, 0, h), vb = page_block(a.c, page, 1, h);
-      const uint8_t* kp = a.c.pool + kb * block_bytes + (g * kPage + c) * 16;
+      kb = page_block(a.c, page, 0, h);
+      vb = page_block(a.c, page, 1, h);
+      kp = a.c.pool + kb * block_bytes + (g * kPage + c) * 16;
       vp = a.c.pool + vb * block_bytes + (g * D + c) * 16;
+    };
+    auto load_k = [&](int s) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int i = 0; i < ND; ++i)
-          kw[s * ND + i] = *reinterpret_cast<const uint4*>(kp + (i * 4 * kPage + 16 * s) * 16);
+      for (int i = 0; i < ND; ++i)
+        kw[s * ND + i] = load16<ONCE>(kp + (i * 4 * kPage + 16 * s) * 16);
+    };
+    auto load_v = [&](int t) { vw[t] = load16<ONCE>(vp + t * 256); };
+    for (int p0 = p_lo + wave; p0 < p_hi; p0 += kWave * kWaves) {
+      // lane i holds the id of the wave's i-th page from here on: no load of an
+      // id, and no wait for one, stands between the pages' loads
+      const int ids = table[min(p0 + kWaves * lane, p_hi - 1)];
+      const int count = min(kWave, (p_hi - p0 + kWaves - 1) / kWaves);
+      find_page(__builtin_amdgcn_readlane(ids, 0));
+      // In the order of the loop's loads: a wait is for the oldest loads, and
+      // the compiler allows for both ways into the loop.
       ks8 = a.c.scale[kb];
       vs8 = a.c.scale[vb];
-    };
-    if (p_lo + wave < p_hi) load_page(p_lo + wave);
-    for (int pi = p_lo + wave; pi < p_hi; pi += kWaves) {
-      uint4 vw[4 * ND];
-#pragma unroll
-      for (int t = 0; t < 4 * ND; ++t) vw[t] = *reinterpret_cast<const uint4*>(vp + t * 256);
-      const float ks = a.scale_log2 * e8m0_to_f32(ks8), vs = e8m0_to_f32(vs8);
-      const bool bad_now = bad;
-      f32x4_t sc[4];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        sc[s] = zero;
-#pragma unroll
-        for (int i = 0; i < ND; ++i) {
-          const uint4 w = kw[s * ND + i];
-          sc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(w.x, w.y), qf[2 * i], sc[s],
-                                                          0, 0, 0);
-          sc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(w.z, w.w), qf[2 * i + 1],
-                                                          sc[s], 0, 0, 0);
-        }
-      }
-      if (pi + kWaves < p_hi) load_page(pi + kWaves);
-      const bool edge = pi * kPage + kPage > lim_lo;  // some row does not see all of the page
-      float pm = neg_inf();
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x = sc[s][i] * ks;
-          if (bad_now) x = __uint_as_float(0x7fc00000u);
-          if (edge && pi * kPage + 16 * s + 4 * g + i >= lim) x = neg_inf();
-          sc[s][i] = x;
-          pm = fmaxf(pm, x);
-        }
-      const float mn = fmaxf(m, groups_max(pm));
-      const float ref = mn == neg_inf() ? 0.f : mn;
-      const float alpha = exp2_(m - ref);
-      float ps = 0.f;
-      f16x8_t pf[2];
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = exp2_(sc[s][i] - ref);
-          ps += p;
-          pf[s >> 1][4 * (s & 1) + i] = static_cast<_Float16>(p);
-        }
-      l = l * alpha + ps;
-      m = mn;
-      if (MASS) {
-        const float sum = groups_sum(ps);
-        if (g == 0)
-          a.rec[((static_cast<size_t>(b) * a.c.max_pages + pi) * a.c.Hkv + h) * a.max_rows + r0 +
-                c] = ref + __log2f(sum);
+        load_k(s);
+        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int t = 0; t < 4 * ND; ++t) {
-        uint4 w = vw[t];
-        f32x4_t nan = zero;
-        if (edge) {
-          // a NaN code reaches only the rows that see it: its place is cleared
-          // and counted under the rows' masks
-          uint32_t x[4] = {w.x, w.y, w.z, w.w}, bits = 0;
-          uint32_t nb[4];
+        load_v(t);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      for (int i = 0; i < count; ++i) {
+        const int pi = p0 + i * kWaves;
+        const float vs = e8m0_to_f32(vs8);
+        const float ks = bad ? __uint_as_float(0x7fc00000u) : a.scale_log2 * e8m0_to_f32(ks8);
+        // past the end: the last page again, so that no branch stands around
+        // the loads (the waits below would then be for all of them)
+        find_page(__builtin_amdgcn_readlane(ids, min(i + 1, count - 1)));
+        ks8 = a.c.scale[kb];
+        vs8 = a.c.scale[vb];
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4_t sc[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            nb[k] = nan_bytes(x[k]);
-            bits |= nb[k];
-            x[k] &= ~nb[k];
-          }
-          w = make_uint4(x[0], x[1], x[2], x[3]);
+        for (int s2 = 0; s2 < 4; s2 += 2) {
+          // two tiles at a time: two independent chains of products
+          sc[s2] = sc[s2 + 1] = zero;
+#pragma unroll
+          for (int i = 0; i < ND; ++i)
+#pragma unroll
+            for (int s = s2; s < s2 + 2; ++s) {
+              const uint4 w = kw[s * ND + i];
+              sc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(w.x, w.y), qf[2 * i],
+                                                              sc[s], 0, 0, 0);
+              sc[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(w.z, w.w),
+                                                              qf[2 * i + 1], sc[s], 0, 0, 0);
+            }
+          load_k(s2);
+          load_k(s2 + 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        const bool edge = pi * kPage + kPage > lim_lo;  // some row does not see all of the page
+#pragma unroll
+        for (int s = 0; s < 4; ++s) sc[s] *= ks;
+        if (edge) {
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (pi * kPage + 16 * s + 4 * g + i >= lim) sc[s][i] = neg_inf();
+          // A NaN code of V reaches only the rows that see it: 0 * NaN would
+          // reach all.  Such places (rare) are cleared, and counted under the
+          // rows' masks: a row that sees one is NaN from here on.
+          uint32_t bits = 0;
+#pragma unroll
+          for (int t = 0; t < 4 * ND; ++t)
+            bits |= nan_bytes(vw[t].x) | nan_bytes(vw[t].y) | nan_bytes(vw[t].z) |
+                    nan_bytes(vw[t].w);
           if (__any(bits != 0)) {
             f16x8_t seen[2];
 #pragma unroll
             for (int q = 0; q < 16; ++q)
               seen[q >> 3][q & 7] = static_cast<_Float16>(
                   pi * kPage + 16 * (q >> 2) + 4 * g + (q & 3) < lim ? 1.f : 0.f);
-            // 0x38 is the code of 1
-            nan = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                codes_f16(nb[0] & 0x38383838u, nb[1] & 0x38383838u), seen[0], nan, 0, 0, 0);
-            nan = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                codes_f16(nb[2] & 0x38383838u, nb[3] & 0x38383838u), seen[1], nan, 0, 0, 0);
+#pragma unroll
+            for (int t = 0; t < 4 * ND; ++t) {
+              const uint4 nb = make_uint4(nan_bytes(vw[t].x), nan_bytes(vw[t].y),
+                                          nan_bytes(vw[t].z), nan_bytes(vw[t].w));
+              vw[t] = make_uint4(vw[t].x & ~nb.x, vw[t].y & ~nb.y, vw[t].z & ~nb.z,
+                                 vw[t].w & ~nb.w);
+              constexpr uint32_t kOne = 0x38383838u;  // codes of 1
+              f32x4_t n = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                  codes_f16(nb.x & kOne, nb.y & kOne), seen[0], zero, 0, 0, 0);
+              n = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(nb.z & kOne, nb.w & kOne),
+                                                         seen[1], n, 0, 0, 0);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (n[i] > 0.f) acc[t][i] = __uint_as_float(0x7fc00000u);
+            }
           }
         }
-        f32x4_t o =
-            __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(w.x, w.y), pf[0], zero, 0, 0, 0);
-        o = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(w.z, w.w), pf[1], o, 0, 0, 0);
+        float pm = neg_inf();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[t][i] = fmaf(o[i], vs, acc[t][i] * alpha);
-          if (edge && nan[i] > 0.f) acc[t][i] = __uint_as_float(0x7fc00000u);
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pm = fmaxf(pm, sc[s][i]);
+        const float mn = fmaxf(m, groups_max(pm));
+        const float ref = mn == neg_inf() ? 0.f : mn;
+        const float alpha = exp2_(m - ref);
+        float ps = 0.f;
+        f16x8_t pf[2];
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p = exp2_(sc[s][i] - ref);
+            ps += p;
+            pf[s >> 1][4 * (s & 1) + i] = static_cast<_Float16>(p);
+          }
+        l = l * alpha + ps;
+        m = mn;
+        if (MASS) {
+          const float sum = groups_sum(ps);
+          if (g == 0)
+            a.rec[((static_cast<size_t>(b) * a.c.max_pages + pi) * a.c.Hkv + h) * a.max_rows + r0 +
+                  c] = ref + __log2f(sum);
+        }
+#pragma unroll
+        for (int t2 = 0; t2 < 4 * ND; t2 += 2) {
+#pragma unroll
+          for (int t = t2; t < t2 + 2; ++t) {
+            const uint4 w = vw[t];
+            f32x4_t o =
+                __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(w.x, w.y), pf[0], zero, 0, 0, 0);
+            o = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(w.z, w.w), pf[1], o, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(o[i], vs, acc[t][i] * alpha);
+          }
+          load_v(t2);
+          load_v(t2 + 1);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
@@ -304,31 +357,37 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
       s_l[wave][c] = l;
     }
     __syncthreads();
-    const int row = tid >> 4, q = tid & 15, valid = min(kRows, rows - r0);
+    // A team of sixteen threads holds a row: thread q dimensions 4 q + 64 i.
+    // The row's waves (here) or parts (below) are split over the teams that
+    // the tile's rows leave: rv teams side by side take rows 0 .. rv - 1.
+    const int valid = min(kRows, rows - r0);
+    const int rv = valid > 8 ? 16 : valid > 4 ? 8 : valid > 2 ? 4 : valid > 1 ? 2 : 1;
+    const int team = tid >> 4, q = tid & 15, row = team & (rv - 1), grp = team / rv;
     float mx = s_m[0][row];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) mx = fmaxf(mx, s_m[w][row]);
     const float ref = mx == neg_inf() ? 0.f : mx;  // a part may see no token
-    float f[kWaves], sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      f[w] = exp2_(s_m[w][row] - ref);
-      sum += s_l[w][row] * f[w];
-    }
+    float sum = 0.f;
     f32x4_t o[ND];
 #pragma unroll
-    for (int i = 0; i < ND; ++i) {
-      o[i] = zero;
+    for (int i = 0; i < ND; ++i) o[i] = zero;
+    if (grp == 0 && row < valid) {
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w)
-        o[i] += *reinterpret_cast<const f32x4_t*>(&s_o[w][row][4 * q + 64 * i]) * f[w];
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = exp2_(s_m[w][row] - ref);
+        sum += s_l[w][row] * f;
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+          o[i] += *reinterpret_cast<const f32x4_t*>(&s_o[w][row][4 * q + 64 * i]) * f;
+      }
     }
+    const bool mine = grp == 0 && row < valid;
     const int out_j = (r0 + row) / a.G;
     uint16_t* op = a.out + static_cast<int64_t>(sq.q0 + out_j) * a.out_stride +
                    (static_cast<int64_t>(h) * a.G + r0 + row - out_j * a.G) * D;
     float* lse = a.lse + (static_cast<size_t>(b) * a.c.Hkv + h) * a.max_rows + r0 + row;
     if (p_hi - p_lo == n_pages) {
-      if (row < valid) {
+      if (mine) {
         store_row<ND>(op, q, o, 1.f / sum);
         if (MASS && q == 0) *lse = mx + __log2f(sum);
       }
@@ -337,16 +396,15 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
       const int w0 = first / chunk, w1 = (first + n_pages - 1) / chunk, parts = w1 - w0 + 1;
       const size_t slot0 =
           static_cast<size_t>(blockIdx.y) * (gridDim.x + a.c.B) + w0 + b;  // part 0
-      const size_t mine = slot0 + (blockIdx.x - w0);
-      float* po = a.part_o + mine * kRows * D;
-      if (row < valid) {
+      const size_t slot = slot0 + (blockIdx.x - w0);
+      if (mine) {
+        float* po = a.part_o + (slot * kRows + row) * D + 4 * q;
 #pragma unroll
         for (int i = 0; i < ND; ++i)
-          st_f32x4<true>(po + row * D + 4 * q + 64 * i,
-                         make_float4(o[i][0], o[i][1], o[i][2], o[i][3]));
+          st_f32x4<true>(po + 64 * i, make_float4(o[i][0], o[i][1], o[i][2], o[i][3]));
         if (q == 0) {
-          st_f32<true>(a.part_ml + (mine * kRows + row) * 2, mx);
-          st_f32<true>(a.part_ml + (mine * kRows + row) * 2 + 1, sum);
+          st_f32<true>(a.part_ml + (slot * kRows + row) * 2, mx);
+          st_f32<true>(a.part_ml + (slot * kRows + row) * 2 + 1, sum);
         }
       }
       wait_memory();
@@ -358,41 +416,72 @@ __global__ __launch_bounds__(kThreads, 2) void attend_kernel(AttendArgs a) {
       __syncthreads();
       if (s_last) {
         if (tid == 0) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        const float* ml = a.part_ml + slot0 * kRows * 2;
-        float top = neg_inf();
-        if (row < valid)
-          for (int p = q; p < parts; p += 16)
-            top = fmaxf(top, ld_f32<true>(ml + (p * kRows + row) * 2));
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
-        float total = 0.f;
+        // Plain loads: no workgroup has read a slot's lines in this launch
+        // before they were written through.
+        const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + slot0 * kRows;
+        // Each team takes every step-th part of its row, a part's weight and
+        // values loaded together (one trip to memory), in a running softmax.
+        const int step = kTeams / rv;  // teams per row
+        float top = neg_inf(), total = 0.f;
 #pragma unroll
         for (int i = 0; i < ND; ++i) o[i] = zero;
-        for (int p0 = 0; p0 < parts; p0 += kJoin) {
-          const int np = min(kJoin, parts - p0);
-          __syncthreads();
-          if (row < valid)
-            for (int p = q; p < np; p += 16) {
-              const float* x = ml + ((p0 + p) * kRows + row) * 2;
-              const float w = exp2_(ld_f32<true>(x) - top);
-              s_f[p][row] = w;
-              total += ld_f32<true>(x + 1) * w;
-            }
-          __syncthreads();
-          if (row < valid)
-            for (int p = 0; p < np; ++p) {
-              const float w = s_f[p][row];
-              const float* x = a.part_o + ((slot0 + p0 + p) * kRows + row) * D + 4 * q;
-#pragma unroll
-              for (int i = 0; i < ND; ++i) {
-                const float4 y = ld_f32x4<true>(x + 64 * i);
-                o[i] += f32x4_t{y.x, y.y, y.z, y.w} * w;
-              }
-            }
-        }
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1) total += __shfl_xor(total, off, kWave);
         if (row < valid) {
+          const float* base = a.part_o + (slot0 * kRows + row) * D + 4 * q;
+          for (int p0 = grp; p0 < parts; p0 += kJoin * step) {
+            float2 x[kJoin];
+            float4 y[kJoin][ND];
+#pragma unroll
+            for (int k = 0; k < kJoin; ++k) {
+              const int p = min(p0 + k * step, parts - 1);  // past the end: not used
+              x[k] = ml[p * kRows + row];
+#pragma unroll
+              for (int i = 0; i < ND; ++i)
+                y[k][i] = *reinterpret_cast<const float4*>(base + static_cast<size_t>(p) * kRows * D +
+                                                           64 * i);
+            }
+            const float old = top;
+#pragma unroll
+            for (int k = 0; k < kJoin; ++k) top = fmaxf(top, x[k].x);
+            const float r = top == neg_inf() ? 0.f : top;
+            const float alpha = exp2_(old - r);
+            total *= alpha;
+#pragma unroll
+            for (int i = 0; i < ND; ++i) o[i] *= alpha;
+#pragma unroll
+            for (int k = 0; k < kJoin; ++k) {
+              if (p0 + k * step >= parts) break;
+              const float w = exp2_(x[k].x - r);
+              total += x[k].y * w;
+#pragma unroll
+              for (int i = 0; i < ND; ++i)
+                o[i] += f32x4_t{y[k][i].x, y[k][i].y, y[k][i].z, y[k][i].w} * w;
+            }
+          }
+        }
+        // the row's teams in order
+        if (row < valid) {
+#pragma unroll
+          for (int i = 0; i < ND; ++i)
+            *reinterpret_cast<f32x4_t*>(&s_j[team][4 * q + 64 * i]) = o[i];
+          if (q == 0) {
+            s_j[team][D] = total;
+            s_j[team][D + 1] = top;
+          }
+        }
+        __syncthreads();
+        if (mine) {
+          for (int k = 1; k < step; ++k) top = fmaxf(top, s_j[k * rv + row][D + 1]);
+          total = 0.f;
+#pragma unroll
+          for (int i = 0; i < ND; ++i) o[i] = zero;
+          for (int k = 0; k < step; ++k) {
+            const float* x = s_j[k * rv + row];
+            const float w = exp2_(x[D + 1] - top);
+#pragma unroll
+            for (int i = 0; i < ND; ++i)
+              o[i] += *reinterpret_cast<const f32x4_t*>(x + 4 * q + 64 * i) * w;
+            total += x[D] * w;
+          }
           store_row<ND>(op, q, o, 1.f / total);
           if (MASS && q == 0) *lse = top + __log2f(total);
         }
@@ -425,8 +514,10 @@ __global__ __launch_bounds__(kThreads) void mass_kernel(AttendArgs a) {
 template <int ND>
 hipError_t launch(const AttendArgs& a, hipStream_t s) {
   const dim3 grid(a.workers, a.c.Hkv * (a.max_rows / kRows));
-  if (a.mass_out) hipLaunchKernelGGL((attend_kernel<ND, true>), grid, dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((attend_kernel<ND, false>), grid, dim3(kThreads), 0, s, a);
+  const bool once = a.max_rows == kRows;
+  auto* k = a.mass_out ? (once ? attend_kernel<ND, true, true> : attend_kernel<ND, true, false>)
+                       : (once ? attend_kernel<ND, false, true> : attend_kernel<ND, false, false>);
+  hipLaunchKernelGGL(k, grid, dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
