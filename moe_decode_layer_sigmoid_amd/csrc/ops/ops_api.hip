@@ -207,9 +207,17 @@ int moe_decode_product_plan(const moe_decode_product_desc* d, int device,
   int rc = moe_decode_product_desc_check(d);
   if (rc) return rc;
   void* ws = nullptr;
-  const size_t bytes = 0;
+  const size_t bytes = moe::product_workspace(d->max_rows, d->n, d->k,
+                                              d->out_fmt == MOE_DECODE_OUT_FP32);
   rc = plan_workspace(device, bytes, &ws);
   if (rc) return rc;
+  {
+    DeviceScope dev(device);
+    if (!dev.ok() || moe::product_prepare() != hipSuccess) {
+      free_workspace(device, ws);
+      return MOE_DECODE_ERR_HIP;
+    }
+  }
   auto* p = new (std::nothrow) moe_decode_product_plan_s{*d, device, ws, bytes};
   if (!p) {
     free_workspace(device, ws);
@@ -238,7 +246,9 @@ int moe_decode_product_run(moe_decode_product_plan_t p, const moe_decode_product
   k.K = p->desc.k;
   k.e8m0 = p->desc.scale_fmt == MOE_DECODE_SCALE_E8M0;
   k.f32 = p->desc.out_fmt == MOE_DECODE_OUT_FP32;
-  return status(moe::launch_product(k, static_cast<hipStream_t>(stream)));
+  const int elem = k.f32 ? 4 : 2;
+  k.wide = aligned(k.out, 4 * elem) && k.ld % 4 == 0;
+  return status(moe::launch_product(k, p->ws, p->ws_bytes, static_cast<hipStream_t>(stream)));
 }
 
 int moe_decode_product_destroy(moe_decode_product_plan_t p) {

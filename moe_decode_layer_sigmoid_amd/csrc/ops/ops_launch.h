@@ -25,8 +25,17 @@ struct ProductArgs {
   int64_t ld;
   int M, N, K;
   bool e8m0, f32;
+  bool wide;  // four outputs may be stored at once
+  // (set by launch_product)
+  int splits;       // workgroups that share out a tile's columns
+  float* part;      // [tiles][splits] tiles of sums
+  uint32_t* count;  // [tiles] parts handed in; 0 between runs
 };
-hipError_t launch_product(const ProductArgs& a, hipStream_t s);
+// Bytes that products of up to max_rows rows need, zeroed before the first.
+size_t product_workspace(int max_rows, int N, int K, bool f32);
+// Once per device (current), before the first launch.
+hipError_t product_prepare();
+hipError_t launch_product(const ProductArgs& a, void* ws, size_t ws_bytes, hipStream_t s);
 
 // ---- cache --------------------------------------------------------------------
 // The cache as the kernels see it.

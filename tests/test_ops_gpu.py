@@ -108,7 +108,9 @@ def check_product(codes, scales, w, ws, out, half):
 
 SHAPES = [(1, 16, 128), (1, 4096, 4096), (2, 17, 256), (7, 1, 384), (16, 129, 1280), (33, 1000, 640),
           (64, 2047, 2048), (65, 640, 256), (129, 257, 896), (200, 384, 128), (255, 511, 512),
-          (300, 1030, 1152), (520, 777, 256), (1, 31, 65536)]
+          (300, 1030, 1152), (520, 777, 256), (1, 31, 65536),
+          # few tiles and many columns (split), large tiles with ragged edges
+          (20, 300, 6144), (100, 1000, 4096), (12, 7000, 1024), (900, 4000, 384), (4000, 4090, 384)]
 
 
 @pytest.mark.parametrize("fmt", ["fp32", "e8m0"])
