@@ -44,7 +44,7 @@ extern "C" {
  * x as it is.  K a multiple of 128, at most 65536; M at most 2^20; x_stride a
  * multiple of 8, at least the columns.
  * Errors: INVALID_ARG (null or misaligned pointer (x: 16 bytes, codes: 8), negative size,
- * limit negative or NaN, a stride too small or no multiple of 8), UNSUPPORTED (sizes), HIP.
+ * limit negative, NaN or above 10^18, a stride too small or no multiple of 8), UNSUPPORTED (sizes), HIP.
  */
 int moe_decode_quant(const void* x, int64_t x_stride, int32_t M, int32_t K, float limit,
                      void* codes, void* scales, void* stream);

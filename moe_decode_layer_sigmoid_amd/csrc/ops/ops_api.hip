@@ -157,7 +157,7 @@ extern "C" {
 
 int moe_decode_quant(const void* x, int64_t x_stride, int32_t M, int32_t K, float limit,
                      void* codes, void* scales, void* stream) {
-  if (!x || !codes || !scales || M < 0 || K <= 0 || !(limit >= 0.f))
+  if (!x || !codes || !scales || M < 0 || K <= 0 || !(limit >= 0.f && limit <= 1e18f))
     return MOE_DECODE_ERR_INVALID_ARG;
   const int64_t cols = limit > 0.f ? 2 * static_cast<int64_t>(K) : K;
   if (!aligned(x, 16) || !aligned(codes, 8) || x_stride < cols || x_stride % 8)

@@ -8,13 +8,11 @@ namespace moe {
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
-// e of the least power of two with amax <= 448 * 2^e, at least -127
-// (448 = 0.875 * 2^9; amax finite and not negative).
+// e of the least power of two with amax <= 448 * 2^e, at least -127 (amax
+// finite and not negative).  448 = 1.75 * 2^8: a mantissa above 1.75 carries
+// into the exponent.
 __device__ __forceinline__ int scale_exp(float amax) {
-  if (amax == 0.f) return -127;
-  int ex;
-  const float m = frexpf(amax, &ex);
-  return max(ex - (m <= 0.875f ? 9 : 8), -127);
+  return max(static_cast<int>((__float_as_uint(amax) + 0x1fffffu) >> 23) - 135, -127);
 }
 
 // 2^e as a float, e in [-149, 127].

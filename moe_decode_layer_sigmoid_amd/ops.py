@@ -12,6 +12,7 @@ A tensor that was made on another stream is the caller's to order and to keep.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 from .binding import ERR_INVALID_ARG, MoeDecodeError, SCALE_E8M0, SCALE_FP32, lib
 
@@ -55,6 +56,14 @@ class EvictArgs(ctypes.Structure):
         (n, _i32) for n in ("keep", "sink", "recent")]
 
 
+# The argument structs as one call makes them: packing costs a quarter of
+# filling a ctypes.Structure.
+_pack_product = struct.Struct("5Qq").pack
+_pack_append = struct.Struct("5Q2Q2q").pack
+_pack_attend = struct.Struct("5QQqQqf4x2Q").pack
+_pack_evict = struct.Struct("8Q3i4x").pack
+
+
 def declare(L) -> None:
     """The prototypes of include/moe_decode_ops.h on the loaded library."""
     P = ctypes.POINTER
@@ -63,17 +72,18 @@ def declare(L) -> None:
         "product_desc_check": [P(ProductDesc)],
         "product_args_check": [P(ProductDesc), P(ProductArgs), _i32],
         "product_plan": [P(ProductDesc), ctypes.c_int, P(_vp)],
-        "product_run": [_vp, P(ProductArgs), _i32, _vp],
-        "product_destroy": [_vp],
+                "product_destroy": [_vp],
         "cache_desc_check": [P(CacheDesc)],
         "append_check": [P(CacheDesc), P(AppendArgs), _i32, _i32],
         "attend_check": [P(CacheDesc), P(AttendArgs), _i32, _i32],
         "evict_check": [P(CacheDesc), P(EvictArgs), _i32],
         "cache_plan": [P(CacheDesc), ctypes.c_int, P(_vp)],
         "cache_destroy": [_vp],
-        "cache_append": [_vp, P(AppendArgs), _i32, _i32, _vp],
-        "cache_attend": [_vp, P(AttendArgs), _i32, _i32, _vp],
-        "cache_evict": [_vp, P(EvictArgs), _i32, _vp],
+        # the arguments as a pointer or as packed bytes
+        "product_run": [_vp, _vp, _i32, _vp],
+        "cache_append": [_vp, _vp, _i32, _i32, _vp],
+        "cache_attend": [_vp, _vp, _i32, _i32, _vp],
+        "cache_evict": [_vp, _vp, _i32, _vp],
     }
     for name, args in protos.items():
         f = getattr(L, "moe_decode_" + name)
@@ -83,57 +93,70 @@ def declare(L) -> None:
         f.argtypes, f.restype = [_vp], ctypes.c_size_t
 
 
-def _need(ok: bool, what: str, why: str) -> None:
+def _need(ok: bool, what: str, why: str, *args) -> None:
     if not ok:
-        raise MoeDecodeError(ERR_INVALID_ARG, "%s: %s" % (what, why))
+        raise MoeDecodeError(ERR_INVALID_ARG, "%s: %s" % (what, why % args))
 
 
 def _tensor(what, name, t, dtypes, shape, device) -> int:
     """The address of a contiguous tensor of one of `dtypes` and `shape` on
     CUDA device `device`."""
-    if t.get_device() != device or t.dtype not in dtypes or tuple(t.shape) != shape \
-            or not t.is_contiguous():
-        raise MoeDecodeError(ERR_INVALID_ARG, "%s: %s must be a contiguous %s tensor %s on device "
-                             "%d, got %s %s on %s" % (what, name, "/".join(str(d) for d in dtypes),
-                                                      list(shape), device, t.dtype,
-                                                      list(t.shape), t.device))
-    return t.data_ptr()
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    raise MoeDecodeError(ERR_INVALID_ARG, "%s: %s must be a contiguous %s tensor %s on device "
+                         "%d, got %s %s strides %s on %s"
+                         % (what, name, "/".join(str(d) for d in dtypes), list(shape), device,
+                            t.dtype, list(t.shape), list(t.stride()), t.device))
+
+
+def _rows(what, name, t, dtypes, shape, device) -> int:
+    """As _tensor for at least shape[0] rows."""
+    if t.dtype in dtypes and t.get_device() == device and t.is_contiguous():
+        s = t.shape
+        if s == shape or (len(s) == len(shape) and s[0] > shape[0] and s[1:] == shape[1:]):
+            return t.data_ptr()
+    return _tensor(what, name, t, dtypes, shape, device)
 
 
 # torch and the types of the operators' tensors, set at the first use: the
 # package itself loads without torch.
 torch = None
+_raw_stream = None  # device -> its current stream's handle
 _CODES = _BYTES = _BF16 = _I32 = _F32 = ()
 
 
 def _load_torch() -> None:
-    global torch, _CODES, _BYTES, _BF16, _I32, _F32
+    global torch, _raw_stream, _CODES, _BYTES, _BF16, _I32, _F32
     if torch is None:
         import torch as t
 
         _CODES, _BYTES = (t.uint8, t.float8_e4m3fn), (t.uint8,)
         _BF16 = (t.bfloat16, t.int16)  # int16: bf16 bit patterns
         _I32, _F32 = (t.int32,), (t.float32,)
+        # without the Stream object that torch.cuda.current_stream makes (1 us)
+        _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream",
+                              lambda d: t.cuda.current_stream(d).cuda_stream)
         torch = t
 
 
 def _heads(what, name, t, T, heads, D, device):
     """(address, token stride) of a [>= T, heads, D] bf16 tensor whose tokens
     may be strided."""
-    if t.get_device() != device or t.dtype not in _BF16 or t.dim() != 3 or t.shape[0] < T \
-            or t.shape[1] != heads or t.shape[2] != D or t.stride(2) != 1 \
-            or (heads > 1 and t.stride(1) != D):
-        raise MoeDecodeError(ERR_INVALID_ARG, "%s: %s must be a bf16 tensor [%d, %d, %d] on device "
-                             "%d with contiguous tokens, got %s %s strides %s on %s"
-                             % (what, name, T, heads, D, device, t.dtype, list(t.shape),
-                                list(t.stride()), t.device))
-    # one token: its stride means nothing
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * D
+    if t.dim() == 3 and t.dtype in _BF16 and t.get_device() == device:
+        n, h, d = t.shape
+        s0, s1, s2 = t.stride()
+        if n >= T and h == heads and d == D and s2 == 1 and (s1 == D or heads == 1):
+            # one token: its stride means nothing
+            return t.data_ptr(), s0 if n > 1 else heads * D
+    raise MoeDecodeError(ERR_INVALID_ARG, "%s: %s must be a bf16 tensor [%d, %d, %d] on device "
+                         "%d with contiguous tokens, got %s %s strides %s on %s"
+                         % (what, name, T, heads, D, device, t.dtype, list(t.shape),
+                            list(t.stride()), t.device))
 
 
 def _stream_of(stream, device: int) -> int:
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _raw_stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -149,26 +172,28 @@ def quant(x, codes, scales, limit=None, stream=None) -> None:
     what = "moe_decode_quant"
     _load_torch()
     device = codes.get_device()
-    _need(codes.dim() == 2 and x.dim() == 2, what, "x and codes must be matrices")
+    _need(device >= 0, what, "tensors must be on a GPU")
+    _need(codes.dim() == 2, what, "codes must be a matrix")
+    _need(limit is None or limit > 0, what, "limit must be positive")
     M, K = codes.shape
     cols = K if limit is None else 2 * K
-    _need(limit is None or limit > 0, what, "limit must be positive")
-    _need(x.get_device() == device and x.dtype in _BF16 and tuple(x.shape) == (M, cols)
-          and (x.stride(1) == 1 or cols == 1), what,
-          "x must be a bf16 tensor [%d, %d] on the device of codes with contiguous rows" % (M, cols))
-    _need(device >= 0, what, "tensors must be on a GPU")
+    if not (x.dtype in _BF16 and x.shape == (M, cols) and x.get_device() == device
+            and x.stride(1) == 1):
+        _need(False, what, "x must be a bf16 tensor [%d, %d] on the device of codes with "
+              "contiguous rows", M, cols)
     pc = _tensor(what, "codes", codes, _CODES, (M, K), device)
     ps = _tensor(what, "scales", scales, _BYTES, (M, K // 128), device)
     if M == 0:
         return
-    xs = x.stride(0) if M > 1 else cols
-    L, s = lib(), _stream_of(stream, device)
+    args = (x.data_ptr(), x.stride(0) if M > 1 else cols, M, K, limit or 0.0, pc, ps,
+            _stream_of(stream, device))
     if device == torch.cuda.current_device():
-        rc = L.moe_decode_quant(x.data_ptr(), xs, M, K, limit or 0.0, pc, ps, s)
+        rc = lib().moe_decode_quant(*args)
     else:
         with torch.cuda.device(device):
-            rc = L.moe_decode_quant(x.data_ptr(), xs, M, K, limit or 0.0, pc, ps, s)
-    _done(rc, what)
+            rc = lib().moe_decode_quant(*args)
+    if rc:
+        _done(rc, what)
 
 
 def make_product_desc(N, K, max_rows, scale_fmt="fp32", out_fmt="bf16") -> ProductDesc:
@@ -191,9 +216,10 @@ class _PlanBase:
         _load_torch()
         self.desc = desc
         self.device = device
+        self._lib = lib()
         self._h = ctypes.c_void_p()
         what = "moe_decode_%s_plan" % self._kind
-        _done(getattr(lib(), what)(ctypes.byref(desc), device, ctypes.byref(self._h)), what)
+        _done(getattr(self._lib, what)(ctypes.byref(desc), device, ctypes.byref(self._h)), what)
 
     def close(self):
         if self._h:
@@ -219,31 +245,35 @@ class ProductPlan(_PlanBase):
 
     _kind = "product"
 
+    def __init__(self, desc, device: int = 0):
+        super().__init__(desc, device)
+        d = self.desc
+        self._N, self._K, self._M = d.n, d.k, d.max_rows
+        self._scale = ((d.n + 127) // 128, d.k // 128)
+        self._scale_types = _F32 if d.scale_fmt == SCALE_FP32 else _BYTES
+        self._out_types = _F32 if d.out_fmt == OUT_FP32 else _BF16
+
     def run(self, M: int, *, codes, scales, w, w_scale, out, stream=None) -> None:
         """out [M, n] = (scales codes) (w_scale w)^T for the first M rows of
         codes, scales and out (whose rows may be strided)."""
-        what, d, dev = "moe_decode_product_run", self.desc, self.device
-        N, K = d.n, d.k
-        _need(0 <= M <= d.max_rows, what, "M must be in [0, %d]" % d.max_rows)
-        want = torch.float32 if d.out_fmt == OUT_FP32 else torch.bfloat16
-        _need(out.get_device() == dev and out.dim() == 2 and out.shape[0] >= M and out.shape[1] == N
-              and (out.dtype == want or (want is torch.bfloat16 and out.dtype == torch.int16))
-              and (out.stride(1) == 1 or N == 1),
-              what, "out must be a %s tensor [%d, %d] on device %d with contiguous rows"
-              % (want, M, N, dev))
-        _need(codes.dim() == 2 and codes.shape[0] >= M and scales.dim() == 2
-              and scales.shape[0] >= M, what, "codes and scales must have %d rows" % M)
-        fmt = _F32 if d.scale_fmt == SCALE_FP32 else _BYTES
-        a = ProductArgs(
-            _tensor(what, "codes", codes, _CODES, (codes.shape[0], K), dev),
-            _tensor(what, "scales", scales, _BYTES, (scales.shape[0], K // 128), dev),
-            _tensor(what, "w", w, _CODES, (N, K), dev),
-            _tensor(what, "w_scale", w_scale, fmt, ((N + 127) // 128, K // 128), dev),
-            out.data_ptr(), out.stride(0) if out.shape[0] > 1 else N)
+        what, dev, N, K = "moe_decode_product_run", self.device, self._N, self._K
+        if not 0 <= M <= self._M:
+            _need(False, what, "M must be in [0, %d]", self._M)
+        rows, cols = out.shape if out.dim() == 2 else (-1, -1)
+        if not (rows >= M and cols == N and out.dtype in self._out_types
+                and out.get_device() == dev and (out.stride(1) == 1 or N == 1)):
+            _need(False, what, "out must be a %s tensor [%d, %d] on device %d with contiguous "
+                  "rows", self._out_types[0], M, N, dev)
+        a = _pack_product(_rows(what, "codes", codes, _CODES, (M, K), dev),
+                          _rows(what, "scales", scales, _BYTES, (M, K // 128), dev),
+                          _tensor(what, "w", w, _CODES, (N, K), dev),
+                          _tensor(what, "w_scale", w_scale, self._scale_types, self._scale, dev),
+                          out.data_ptr(), out.stride(0) if rows > 1 else N)
         if M == 0:
             return
-        _done(lib().moe_decode_product_run(self._h, ctypes.byref(a), M, _stream_of(stream, dev)),
-              what)
+        rc = self._lib.moe_decode_product_run(self._h, a, M, _stream_of(stream, dev))
+        if rc:
+            _done(rc, what)
 
 
 def make_cache_desc(heads, kv_heads, head_dim, pages, max_batch, max_pages, max_q=1,
@@ -276,70 +306,77 @@ class CachePlan(_PlanBase):
 
     _kind = "cache"
 
-    def _cache(self, what, B, pool, pool_scale, page_table, seq_lens, q_start) -> Cache:
-        d, dev = self.desc, self.device
-        _need(0 <= B <= d.max_batch, what, "B must be in [0, %d]" % d.max_batch)
-        _need(page_table.shape[0] >= B and seq_lens.shape[0] >= B and q_start.shape[0] >= B + 1,
-              what, "page_table, seq_lens and q_start must cover %d sequences" % B)
-        return Cache(
-            _tensor(what, "pool", pool, _CODES, (d.pages, 2, d.kv_heads, 64 * d.head_dim), dev),
-            _tensor(what, "pool_scale", pool_scale, _BYTES, (d.pages, 2, d.kv_heads), dev),
-            _tensor(what, "page_table", page_table, _I32, (page_table.shape[0], d.max_pages), dev),
-            _tensor(what, "seq_lens", seq_lens, _I32, (seq_lens.shape[0],), dev),
-            _tensor(what, "q_start", q_start, _I32, (q_start.shape[0],), dev))
+    def __init__(self, desc, device: int = 0):
+        super().__init__(desc, device)
+        d = self.desc
+        self._heads, self._kv, self._D = d.heads, d.kv_heads, d.head_dim
+        self._B, self._P = d.max_batch, d.max_pages
+        self._scale = (d.pages, 2, d.kv_heads)
+        self._pool = self._scale + (PAGE_TOKENS * d.head_dim,)
+
+    def _cache(self, what, B, T, pool, pool_scale, page_table, seq_lens, q_start):
+        dev = self.device
+        if not (0 <= B <= self._B and T >= 0):
+            _need(False, what, "B must be in [0, %d] and T not negative", self._B)
+        return (_tensor(what, "pool", pool, _CODES, self._pool, dev),
+                _tensor(what, "pool_scale", pool_scale, _BYTES, self._scale, dev),
+                _rows(what, "page_table", page_table, _I32, (B, self._P), dev),
+                _rows(what, "seq_lens", seq_lens, _I32, (B,), dev),
+                _rows(what, "q_start", q_start, _I32, (B + 1,), dev))
 
     def append(self, B: int, T: int, *, k, v, pool, pool_scale, page_table, seq_lens, q_start,
                stream=None) -> None:
         """moe_decode_cache_append: K and V [T, kv_heads, head_dim] of the new
         tokens into their pages."""
-        what, d, dev = "moe_decode_cache_append", self.desc, self.device
-        c = self._cache(what, B, pool, pool_scale, page_table, seq_lens, q_start)
-        pk, sk = _heads(what, "k", k, T, d.kv_heads, d.head_dim, dev)
-        pv, sv = _heads(what, "v", v, T, d.kv_heads, d.head_dim, dev)
+        what, dev = "moe_decode_cache_append", self.device
+        c = self._cache(what, B, T, pool, pool_scale, page_table, seq_lens, q_start)
+        pk, sk = _heads(what, "k", k, T, self._kv, self._D, dev)
+        pv, sv = _heads(what, "v", v, T, self._kv, self._D, dev)
         if B == 0 or T == 0:
             return
-        a = AppendArgs(c, pk, pv, sk, sv)
-        _done(lib().moe_decode_cache_append(self._h, ctypes.byref(a), B, T,
-                                            _stream_of(stream, dev)), what)
+        rc = self._lib.moe_decode_cache_append(self._h, _pack_append(*c, pk, pv, sk, sv), B, T,
+                                               _stream_of(stream, dev))
+        if rc:
+            _done(rc, what)
 
     def attend(self, B: int, T: int, *, q, pool, pool_scale, page_table, seq_lens, q_start, out,
                sm_scale, mass_in=None, mass_out=None, stream=None) -> None:
         """moe_decode_cache_attend: out [T, heads, head_dim] of the queries q
         over the cache, and with mass_out the pages' accumulated weight."""
-        what, d, dev = "moe_decode_cache_attend", self.desc, self.device
-        c = self._cache(what, B, pool, pool_scale, page_table, seq_lens, q_start)
-        pq, sq = _heads(what, "q", q, T, d.heads, d.head_dim, dev)
-        po, so = _heads(what, "out", out, T, d.heads, d.head_dim, dev)
-        mi = mo = None
+        what, dev = "moe_decode_cache_attend", self.device
+        c = self._cache(what, B, T, pool, pool_scale, page_table, seq_lens, q_start)
+        pq, sq = _heads(what, "q", q, T, self._heads, self._D, dev)
+        po, so = _heads(what, "out", out, T, self._heads, self._D, dev)
+        mi = mo = 0
         if mass_in is not None:
-            _need(mass_in.shape[0] >= B, what, "mass_in must cover %d sequences" % B)
-            mi = _tensor(what, "mass_in", mass_in, _F32, (mass_in.shape[0], d.max_pages), dev)
+            mi = _rows(what, "mass_in", mass_in, _F32, (B, self._P), dev)
         if mass_out is not None:
-            _need(mass_out.shape[0] >= B, what, "mass_out must cover %d sequences" % B)
-            mo = _tensor(what, "mass_out", mass_out, _F32, (mass_out.shape[0], d.max_pages), dev)
-        if B == 0 or (T == 0 and mo is None):
+            mo = _rows(what, "mass_out", mass_out, _F32, (B, self._P), dev)
+        if B == 0 or (T == 0 and not mo):
             return
-        a = AttendArgs(c, pq, sq, po, so, sm_scale, mi, mo)
-        _done(lib().moe_decode_cache_attend(self._h, ctypes.byref(a), B, T,
-                                            _stream_of(stream, dev)), what)
+        rc = self._lib.moe_decode_cache_attend(
+            self._h, _pack_attend(*c, pq, sq, po, so, sm_scale, mi, mo), B, T,
+            _stream_of(stream, dev))
+        if rc:
+            _done(rc, what)
 
     def evict(self, B: int, keep: int, *, sink, recent, page_table, seq_lens, mass, out_table,
               out_lens, out_mass, freed, n_freed, stream=None) -> None:
         """moe_decode_cache_evict: the pages that each sequence keeps."""
-        what, d, dev = "moe_decode_cache_evict", self.desc, self.device
-        _need(0 <= B <= d.max_batch, what, "B must be in [0, %d]" % d.max_batch)
-        ptrs = []
-        for name, t, dt, wide in (("page_table", page_table, _I32, True),
-                                  ("seq_lens", seq_lens, _I32, False), ("mass", mass, _F32, True),
-                                  ("out_table", out_table, _I32, True),
-                                  ("out_lens", out_lens, _I32, False),
-                                  ("out_mass", out_mass, _F32, True), ("freed", freed, _I32, True),
-                                  ("n_freed", n_freed, _I32, False)):
-            _need(t.shape[0] >= B, what, "%s must cover %d sequences" % (name, B))
-            ptrs.append(_tensor(what, name, t, dt,
-                                (t.shape[0], d.max_pages) if wide else (t.shape[0],), dev))
+        what, dev = "moe_decode_cache_evict", self.device
+        if not 0 <= B <= self._B:
+            _need(False, what, "B must be in [0, %d]", self._B)
+        table, row = (B, self._P), (B,)
+        a = _pack_evict(_rows(what, "page_table", page_table, _I32, table, dev),
+                        _rows(what, "seq_lens", seq_lens, _I32, row, dev),
+                        _rows(what, "mass", mass, _F32, table, dev),
+                        _rows(what, "out_table", out_table, _I32, table, dev),
+                        _rows(what, "out_lens", out_lens, _I32, row, dev),
+                        _rows(what, "out_mass", out_mass, _F32, table, dev),
+                        _rows(what, "freed", freed, _I32, table, dev),
+                        _rows(what, "n_freed", n_freed, _I32, row, dev), keep, sink, recent)
         if B == 0:
             return
-        a = EvictArgs(*ptrs, keep, sink, recent)
-        _done(lib().moe_decode_cache_evict(self._h, ctypes.byref(a), B, _stream_of(stream, dev)),
-              what)
+        rc = self._lib.moe_decode_cache_evict(self._h, a, B, _stream_of(stream, dev))
+        if rc:
+            _done(rc, what)

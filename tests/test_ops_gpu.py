@@ -65,6 +65,28 @@ def test_quant_borders_and_special_values():
     assert scales.equal(rs) and oh.same_codes(codes, rc)
 
 
+def test_quant_swiglu_borders():
+    """Gates and values whose SwiGLU is tiny, huge, zero or next to a border:
+    the codes and scales of 64 bits."""
+    g = gen(12)
+    M, K = 64, 512
+    x = torch.randn(M, 2 * K, generator=g)
+    x[:16, :K] = x[:16, :K] * 30          # far gates
+    x[16:24, :K] = -80 - 20 * torch.rand(8, K, generator=g)  # all but zero
+    x[24:28, :K] = -3e38
+    x[28:32, K:] *= 1e-30
+    x[32:34] = 0
+    x[34:40, :K] = 100.0                  # silu(7) u: one value per u
+    x[40:48, K:] = torch.randint(-8, 9, (8, K), generator=g).float()
+    x[48:56, :K] = torch.randint(-8, 9, (8, K), generator=g).float()
+    x[56:60, 5], x[60:62, K + 5], x[62:, 7] = math.inf, -math.inf, math.nan
+    x = x.to(torch.bfloat16)
+    for limit in (7.0, 0.5, 1e18):
+        codes, scales = run_quant(x.cuda(), K, limit)
+        rc, rs = oh.quant_ref(x, limit)
+        assert scales.equal(rs) and oh.same_codes(codes, rc), limit
+
+
 def test_quant_strided_rows():
     x = torch.randn(7, 1000, generator=gen(3)).to(torch.bfloat16).cuda()
     for v, K, limit in ((x[:, 8:8 + 512], 512, None), (x[::2, 16:16 + 768], 384, 7.0)):

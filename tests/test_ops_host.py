@@ -17,7 +17,7 @@ P = 0x10000  # stands for an aligned device pointer; checks do not dereference
 
 @pytest.mark.parametrize("kw,code", [
     (dict(x=None), BAD), (dict(codes=None), BAD), (dict(scales=None), BAD), (dict(M=-1), BAD),
-    (dict(K=0), BAD), (dict(limit=-1.0), BAD), (dict(limit=math.nan), BAD), (dict(x=P + 8), BAD),
+    (dict(K=0), BAD), (dict(limit=-1.0), BAD), (dict(limit=math.nan), BAD), (dict(limit=1e19, stride=512), BAD), (dict(x=P + 8), BAD),
     (dict(codes=P + 4), BAD), (dict(stride=255), BAD), (dict(stride=260), BAD),
     (dict(limit=7.0, stride=264), BAD), (dict(K=100, stride=256), UNS),
     (dict(K=65664, stride=65664), UNS), (dict(M=(1 << 20) + 1), UNS), (dict(M=0), OK),
@@ -162,3 +162,23 @@ def test_cache_null():
     assert lib.moe_decode_cache_evict(None, None, 1, None) == BAD
     assert lib.moe_decode_cache_destroy(None) == OK
     assert lib.moe_decode_cache_workspace_bytes(None) == 0
+
+
+def test_packed_arguments_are_the_structs():
+    from moe_decode_layer_sigmoid_amd import ops
+
+    def fields(s):
+        for name, kind in s._fields_:
+            v = getattr(s, name)
+            if isinstance(v, ctypes.Structure):
+                yield from fields(v)
+            else:
+                yield v
+
+    for pack, kind, n in ((ops._pack_product, ops.ProductArgs, 6),
+                          (ops._pack_append, ops.AppendArgs, 9),
+                          (ops._pack_attend, ops.AttendArgs, 12),
+                          (ops._pack_evict, ops.EvictArgs, 11)):
+        b = pack(*range(1, n + 1))
+        assert len(b) == ctypes.sizeof(kind)
+        assert list(fields(kind.from_buffer_copy(b))) == list(range(1, n + 1))
