@@ -1,10 +1,16 @@
 // Eviction of whole pages by accumulated attention weight.
 //
 // One workgroup per sequence.  The pages between the first `sink` and the last
-// `recent` compete by a key that orders as their mass does; a radix select
-// (four rounds of a 256-bin count, most significant byte first) finds the key
-// T of the last page that stays and how many pages of key T do; then one pass
-// in page order moves kept and dropped pages to the front of their outputs.
+// `recent` compete by a key that orders as their mass does.  A radix select
+// from the highest bit in which the keys differ finds a key T and a number of
+// ties: the pages above T stay, and the first `ties` of key T.  Its rounds of a
+// 256-bin count end as soon as whole bins stay.  Then one pass in page order
+// moves kept and dropped pages to the front of their outputs.
+//
+// Bound by its own chain of waits: one load, one barrier a round (each wave
+// finds the bin by itself, each round has bins of its own) and one for every
+// 1024 pages that move.  64 sequences of 1024 pages: 5.9 us; with rounds from
+// the top bit down, two scans a round and keys read again 9.8 us.
 #include "ops_device.h"
 #include "ops_launch.h"
 
@@ -13,6 +19,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
+constexpr int kPer = 4;  // pages of a thread, one behind the other
+constexpr int kChunk = kThreads * kPer;
 
 // Order-preserving bits of a float (-0 as 0); NaN above everything.
 __device__ __forceinline__ uint32_t key_of(float f) {
@@ -21,100 +29,156 @@ __device__ __forceinline__ uint32_t key_of(float f) {
   return u >> 31 ? ~u : u | 0x80000000u;
 }
 
-// Sum over the threads before this one, and over all (in *total); every
-// thread calls it, *s has kWaves ints.
-__device__ __forceinline__ int scan(int v, int* s, int* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int x = v;
+// Sum over the lanes up to this one.
+__device__ __forceinline__ int wave_scan(int v) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int off = 1; off < kWave; off <<= 1) {
-    const int y = __shfl_up(x, off, kWave);
-    if (lane >= off) x += y;
+    const int y = __shfl_up(v, off, kWave);
+    if (lane >= off) v += y;
   }
-  __syncthreads();  // the last scan's readers are done
-  if (lane == 63) s[wave] = x;
-  __syncthreads();
-  int before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    before += w < wave ? s[w] : 0;
-    all += s[w];
-  }
-  *total = all;
-  return before + x - v;
+  return v;
 }
 
 __global__ __launch_bounds__(kThreads) void evict_kernel(EvictArgs a) {
-  __shared__ int s_scan[kWaves];
-  __shared__ int s_bins[256];
-  __shared__ int s_pick[2];
-  const int b = blockIdx.x, tid = threadIdx.x;
+  __shared__ __align__(16) int s_bins[4][256];
+  __shared__ uint32_t s_min[kWaves], s_max[kWaves];
+  __shared__ int s_scan[2][kWaves];
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const size_t row = static_cast<size_t>(b) * a.max_pages;
+  const float* mass = a.mass + row;
+  const int* table = a.table + row;
+  // the first chunk's pages, whatever the length turns out to be
+  float m0[kPer];
+  int id0[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = kPer * tid + j;
+    m0[j] = i < a.max_pages ? mass[i] : 0.f;
+    id0[j] = i < a.max_pages ? table[i] : -1;
+  }
   const int len = a.lens[b];
   const bool fits = len >= 0 && len <= a.max_pages * kPage;
   const int n = fits ? (len + kPage - 1) / kPage : a.max_pages;
   const int drop = fits ? max(n - a.keep, 0) : 0;
-  // pages [lo, hi) compete; stay of them do
+  // pages [lo, hi) compete; hi - lo - drop of them stay
   const int lo = min(a.sink, n), hi = max(n - a.recent, lo);
-  const int stay = hi - lo - drop;
-  uint32_t T = 0;
-  int ties = 0;  // pages of key T that stay, lowest first
-  if (drop > 0) {
-    uint32_t mask = 0;
-    int want = stay;  // rank (from the largest) of the last page that stays
-    if (want == 0) {
-      T = 0xffffffffu;  // nothing stays: keys above T none, none of key T
-    } else {
-      for (int shift = 24; shift >= 0; shift -= 8) {
-        s_bins[tid] = 0;
-        __syncthreads();
-        for (int i = lo + tid; i < hi; i += kThreads) {
-          const uint32_t k = key_of(a.mass[row + i]);
-          if ((k & mask) == T) atomicAdd(&s_bins[k >> shift & 255], 1);
-        }
-        __syncthreads();
-        // thread tid has bin 255 - tid: bins from the largest down
-        int all;
-        const int mine = s_bins[255 - tid];
-        const int before = scan(mine, s_scan, &all);
-        if (before < want && want <= before + mine) {
-          s_pick[0] = 255 - tid;
-          s_pick[1] = want - before;
-        }
-        __syncthreads();
-        T |= static_cast<uint32_t>(s_pick[0]) << shift;
-        want = s_pick[1];
-        mask |= 0xffu << shift;
+  uint32_t T = 0xffffffffu;  // nothing stays: no key is above, no tie wanted
+  int ties = 0;              // pages of key T that stay, lowest first
+  int want = hi - lo - drop;
+  if (drop > 0 && want > 0) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s_bins[r][tid] = 0;
+    // f(key) of every competing page of this thread
+    const auto each = [&](auto f) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int i = kPer * tid + j;
+        if (i >= lo && i < hi) f(key_of(m0[j]));
       }
+      for (int i = max(lo, kChunk) + tid; i < hi; i += kThreads) f(key_of(mass[i]));
+    };
+    uint32_t least = 0xffffffffu, most = 0;
+    each([&](uint32_t k) {
+      least = min(least, k);
+      most = max(most, k);
+    });
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+      least = min(least, static_cast<uint32_t>(__shfl_xor(static_cast<int>(least), off, kWave)));
+      most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), off, kWave)));
+    }
+    if (lane == 0) {
+      s_min[wave] = least;
+      s_max[wave] = most;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      least = min(least, s_min[w]);
+      most = max(most, s_max[w]);
+    }
+    // bits above `left` are known: the same in all keys that are still in
+    int left = least == most ? 0 : 32 - __clz(static_cast<int>(least ^ most));
+    T = left == 32 ? 0 : most >> left << left;
+    ties = want;
+    for (int r = 0; left > 0; ++r) {
+      const int shift = max(left - 8, 0);
+      const uint32_t digits = (1u << (left - shift)) - 1u;
+      each([&](uint32_t k) {
+        if (left == 32 || (k ^ T) >> left == 0) atomicAdd(&s_bins[r][k >> shift & digits], 1);
+      });
+      __syncthreads();
+      // lane l has bins 255 - 4 l and the three below, the largest first
+      const int4 q = *reinterpret_cast<const int4*>(&s_bins[r][252 - 4 * lane]);
+      const int upto = wave_scan(q.x + q.y + q.z + q.w);
+      const int w1 = upto - q.x, w2 = w1 - q.y, w3 = w2 - q.z, w4 = w3 - q.w;
+      const bool here = w4 < want && want <= upto;
+      const int bin = want <= w3 ? 3 : want <= w2 ? 2 : want <= w1 ? 1 : 0;
+      const int above = bin == 3 ? w4 : bin == 2 ? w3 : bin == 1 ? w2 : w1;
+      const int in_bin = bin == 3 ? q.w : bin == 2 ? q.z : bin == 1 ? q.y : q.x;
+      const int from = __ffsll(static_cast<unsigned long long>(__ballot(here))) - 1;
+      T |= static_cast<uint32_t>(__shfl(252 - 4 * lane + bin, from, kWave)) << shift;
+      want -= __shfl(above, from, kWave);
       ties = want;
+      left = shift;
+      if (want == __shfl(in_bin, from, kWave)) {
+        // the bin stays as a whole: T its lowest key, with all of its ties
+        ties = INT32_MAX;
+        break;
+      }
     }
   }
   int kept = 0, gone = 0, seen = 0;  // so far; seen: pages of key T
-  for (int i0 = 0; i0 < n; i0 += kThreads) {
-    const int i = i0 + tid;
-    const bool in = i < n, rival = in && drop > 0 && i >= lo && i < hi;
-    const float mass = in ? a.mass[row + i] : 0.f;
-    const int id = in ? a.table[row + i] : -1;
-    const uint32_t k = key_of(mass);
-    int total;
-    const bool tie = rival && k == T;
-    const int tie_rank = seen + scan(tie, s_scan, &total);
-    seen += total;
-    const bool keep = in && (!rival || (tie ? tie_rank < ties : k > T));
-    const int at = kept + scan(keep, s_scan, &total);
-    kept += total;
-    const int nin = min(kThreads, n - i0);
-    // every read of this round is done (scan's barriers), so the outputs may
-    // be the inputs: a page never moves back
-    if (keep) {
-      a.out_table[row + at] = id;
-      a.out_mass[row + at] = mass;
-    } else if (in) {
-      a.freed[row + gone + (i - i0) - (at - (kept - total))] = id;
+  for (int i0 = 0, turn = 0; i0 < n; i0 += kChunk, turn ^= 1) {
+    float m[kPer];
+    int id[kPer];
+    bool in[kPer], rival[kPer], tie[kPer];
+    int mine = 0;  // pages that stay without a tie, and ties * 2^16
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = i0 + kPer * tid + j;
+      in[j] = i < n;
+      m[j] = i0 == 0 ? m0[j] : in[j] ? mass[i] : 0.f;
+      id[j] = i0 == 0 ? id0[j] : in[j] ? table[i] : -1;
+      rival[j] = in[j] && drop > 0 && i >= lo && i < hi;
+      const uint32_t k = key_of(m[j]);
+      tie[j] = rival[j] && k == T;
+      rival[j] = rival[j] && k <= T;
+      mine += tie[j] ? 0x10000 : in[j] && !rival[j] ? 1 : 0;
     }
-    gone += nin - total;
+    const int upto = wave_scan(mine);
+    if (lane == 63) s_scan[turn][wave] = upto;
+    // every read of this chunk is done behind this, so the outputs may be the
+    // inputs: a page never moves back
+    __syncthreads();
+    int before = upto - mine, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const int x = s_scan[turn][w];
+      before += w < wave ? x : 0;
+      all += x;
+    }
+    int tied = seen + (before >> 16);
+    int at = kept + (before & 0xffff) + max(min(tied, ties) - min(seen, ties), 0);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = i0 + kPer * tid + j;
+      const bool keep = in[j] && (!rival[j] || (tie[j] && tied < ties));
+      tied += tie[j];
+      if (keep) {
+        a.out_table[row + at] = id[j];
+        a.out_mass[row + at] = m[j];
+      } else if (in[j]) {
+        a.freed[row + i - at] = id[j];
+      }
+      at += keep;
+    }
+    const int now = (all & 0xffff) + min(seen + (all >> 16), ties) - min(seen, ties);
+    seen += all >> 16;
+    kept += now;
+    gone += min(kChunk, n - i0) - now;
   }
-  __syncthreads();
   for (int i = kept + tid; i < a.max_pages; i += kThreads) {
     a.out_table[row + i] = -1;
     a.out_mass[row + i] = 0.f;
