@@ -24,6 +24,14 @@ bounded waits, and the CPU oracle's rate on a bounded sample.  A point whose
 check fails or whose bounded waits gave up makes the line invalid (exit 1).
 
     python bench.py [--workload decode_t1] [--steps K] [--warmup W]
+
+With --attention it measures, instead, whole decode steps of one layer: the
+attention half (quantiser, q k v projection, append to the 8-bit paged cache,
+attention with the pages' weights, eviction, output projection) before the
+decode_t16 layer, and each of those operators alone; one JSON line, checked
+against plain float64 PyTorch.
+
+    python bench.py --attention [--context 4096] [--steps K] [--warmup W]
 """
 
 from __future__ import annotations
@@ -664,6 +672,174 @@ POINTS = ["decode_t1", "decode_t16", "wide_t64_e8m0", "verify_t128"]
 EXTRA_POINTS = ["dense_t16"]
 
 
+# The attention half of the decode_t16 layer: 16 sequences, one new token each.
+ATTN_HEADS, ATTN_KV, ATTN_DIM = 32, 8, 128
+
+
+def measure_attention(args):
+    """The record of --attention: K captured decode steps back to back, each
+    operator of the step alone (its own graph), the checks."""
+    import torch
+
+    import moe_decode_layer_sigmoid_amd as md
+    from synth import WORKLOADS, make_layer
+
+    sh = WORKLOADS["decode_t16"]
+    T, H, heads, kv, D, ctx = sh.T, sh.H, ATTN_HEADS, ATTN_KV, ATTN_DIM, args.context
+    P = -(-ctx // 64)
+    inp = make_layer(sh, seed=0)
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def dev(a):
+        a = np.ascontiguousarray(a)
+        return torch.from_numpy(a.view(np.int16) if a.dtype == np.uint16 else a).to("cuda")
+
+    def zeros(*shape, dtype=torch.bfloat16):
+        return torch.zeros(*shape, dtype=dtype, device="cuda")
+
+    def weights(N, K):
+        w = (torch.randn(N, K, generator=g, device="cuda") * 64).clamp(-448, 448)
+        s = torch.full((-(-N // 128), K // 128), 1 / (64 * math.sqrt(K)), device="cuda")
+        return w.to(torch.float8_e4m3fn), s
+
+    u8, i32, f32 = torch.uint8, torch.int32, torch.float32
+    wide = (heads + 2 * kv) * D
+    qkv_w, qkv_s = weights(wide, H)
+    o_w, o_s = weights(H, heads * D)
+    qkv_plan = md.ProductPlan(md.make_product_desc(wide, H, T))
+    o_plan = md.ProductPlan(md.make_product_desc(H, heads * D, T))
+    pages = T * P
+    cache = md.CachePlan(md.make_cache_desc(heads, kv, D, pages, T, P))
+    moe = md.Plan(md.make_desc(H, sh.E, sh.k, sh.I, sh.Is, T, sh.scale_fmt, md.PATH_AUTO, sh.limit,
+                               sh.rsf, sh.eps), torch.cuda.current_device())
+    layer = {n: dev(getattr(inp, n)) for n in (
+        "router_w", "router_bias", "w13", "w13_scale", "w2", "w2_scale", "sw13", "sw13_scale",
+        "sw2", "sw2_scale", "gamma") if getattr(inp, n) is not None}
+    x = dev(inp.hidden).view(torch.bfloat16)
+    xc, xs = zeros(T, H, dtype=u8), zeros(T, H // 128, dtype=u8)
+    qkv = zeros(T, heads + 2 * kv, D)
+    attn, hidden = zeros(T, heads, D), zeros(T, H)
+    ac, as_ = zeros(T, heads * D, dtype=u8), zeros(T, heads * D // 128, dtype=u8)
+    out, res = zeros(T, H), zeros(T, H)
+    ids, wts = zeros(T, sh.k, dtype=i32), zeros(T, sh.k, dtype=f32)
+    table = torch.randperm(pages, generator=g, device="cuda").to(i32).view(T, P)
+    lens = torch.full((T,), ctx, dtype=i32, device="cuda")
+    pool = zeros(pages, 2, kv, 64 * D, dtype=u8)
+    where = dict(pool=pool, pool_scale=torch.full((pages, 2, kv), 127, dtype=u8, device="cuda"),
+                 page_table=table, seq_lens=lens,
+                 q_start=torch.arange(T + 1, dtype=i32, device="cuda"))
+    for p in range(0, pages, 256):
+        part = torch.randn(min(256, pages - p), 2, kv, 64 * D, generator=g, device="cuda")
+        pool[p:p + 256] = part.to(torch.float8_e4m3fn).view(u8)
+    mass = torch.rand(T, P, generator=g, device="cuda")
+    new_mass, out_mass = torch.zeros_like(mass), torch.zeros_like(mass)
+    out_table, out_lens = torch.zeros_like(table), torch.zeros_like(lens)
+    freed, n_freed = torch.zeros_like(table), torch.zeros_like(lens)
+    q, k, v = qkv[:, :heads], qkv[:, heads:heads + kv], qkv[:, heads + kv:]
+    sm = D ** -0.5
+    parts = {
+        "quant": lambda: md.quant(x, xc, xs),
+        "qkv_product": lambda: qkv_plan.run(T, codes=xc, scales=xs, w=qkv_w, w_scale=qkv_s,
+                                            out=qkv.view(T, wide)),
+        "append": lambda: cache.append(T, T, k=k, v=v, **where),
+        "attend": lambda: cache.attend(T, T, q=q, out=attn, sm_scale=sm, mass_in=mass,
+                                       mass_out=new_mass, **where),
+        "evict": lambda: cache.evict(T, max(P - 1, 2), sink=1, recent=1, page_table=table,
+                                     seq_lens=lens, mass=new_mass, out_table=out_table,
+                                     out_lens=out_lens, out_mass=out_mass, freed=freed,
+                                     n_freed=n_freed),
+        "quant_attention": lambda: md.quant(attn.view(T, heads * D), ac, as_),
+        "o_product": lambda: o_plan.run(T, codes=ac, scales=as_, w=o_w, w_scale=o_s, out=hidden),
+        "moe_layer": lambda: moe.run(T, hidden=hidden.view(torch.int16),
+                                     residual=x.view(torch.int16), out=out.view(torch.int16),
+                                     residual_out=res.view(torch.int16), topk_ids=ids,
+                                     topk_weights=wts, **layer),
+    }
+
+    def step():
+        for f in parts.values():
+            f()
+
+    # ---- checks: the two products and the attention against float64
+    step()
+    torch.cuda.synchronize()
+
+    def power(s):
+        return torch.exp2(s.double() - 127)
+
+    def product(c, s, w, ws):
+        a = c.view(torch.float8_e4m3fn).double() * power(s).repeat_interleave(128, 1)
+        b = w.double() * ws.double().repeat_interleave(128, 0).repeat_interleave(128, 1)
+        return a @ b.t()
+
+    t_, d_ = torch.arange(64, device="cuda")[:, None], torch.arange(D, device="cuda")[None]
+    at = ((d_ // 16 * 64 + t_) * 16 + d_ % 16, (t_ % 16 // 4 * D + d_) * 16 + t_ // 16 * 4 + t_ % 4)
+    want = torch.zeros(T, heads, D, dtype=torch.float64, device="cuda")
+    for b in range(T):
+        kv_ = []
+        for s in range(2):
+            codes = pool[table[b].long(), s][:, :, at[s]]  # pages, kv, 64, D
+            val = codes.view(torch.float8_e4m3fn).double()
+            val *= power(where["pool_scale"][table[b].long(), s])[:, :, None, None]
+            kv_.append(val.transpose(0, 1).reshape(kv, P * 64, D)[:, :ctx])
+        for h in range(heads):
+            p = torch.softmax(kv_[0][h // (heads // kv)] @ q[b, h].double() * sm, 0)
+            want[b, h] = p @ kv_[1][h // (heads // kv)]
+
+    def rel(got, ref):
+        return float((got.double() - ref).norm() / ref.norm())
+
+    check = {"qkv_product": rel(qkv.view(T, wide), product(xc, xs, qkv_w, qkv_s)),
+             "attend": rel(attn, want), "o_product": rel(hidden, product(ac, as_, o_w, o_s)),
+             "mass": abs(float((new_mass - mass).double().sum()) / (T * heads) - 1)}
+    # bf16 rounds by 2^-8 at most; half that on average
+    check["pass"] = bool(max(check.values()) < 2.0 ** -8) and not moe.check_waits()
+    log("check", json.dumps(check))
+
+    # ---- times
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+
+    def timed(f, calls=1):
+        with torch.cuda.stream(stream):
+            f()
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=stream):
+                for _ in range(calls):
+                    f()
+            for _ in range(args.warmup):
+                graph.replay()
+            torch.cuda.synchronize()
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            torch.cuda._sleep(int(2.4e6 * max(5.0, 0.02 * args.steps)))
+            a.record(stream)
+            for _ in range(args.steps):
+                graph.replay()
+            b.record(stream)
+        torch.cuda.synchronize()
+        return a.elapsed_time(b) / args.steps / calls * 1e3
+
+    us = timed(step)
+    # ten calls to a graph: its own start is longer than the short operators
+    alone = {n: round(timed(f, 10), 2) for n, f in parts.items()}
+    cache_bytes = T * ctx * 2 * kv * D
+    return {
+        "metric": "tokens/s of one layer's decode step with its attention", "value":
+            round(T / us * 1e6, 1), "unit": "tokens/s", "n_gpus": 1, "steps": args.steps,
+        "warmup": args.warmup, "ms_per_step": round(us * 1e-3, 6), "higher_is_better": True,
+        "scaling": "weak", "vs_baseline": None,
+        "dtype": "fp8e4m3 weights, activations and cache, bf16 between, f32 accumulate",
+        "data": "synthetic (seeded)",
+        "config": {"workload": "decode_t16 with attention", "tokens": T, "hidden": H,
+                   "heads": heads, "kv_heads": kv, "head_dim": D, "context": ctx,
+                   "experts": sh.E, "top_k": sh.k, "parallelism": "none (1 GPU)",
+                   "weight_copies": 1},
+        "us_alone": alone, "attend_cache_tbps": round(cache_bytes / alone["attend"] * 1e-6, 3),
+        "check": check, "valid": check["pass"],
+    }
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--gpus", type=int, default=1)
@@ -699,6 +875,11 @@ def main():
     ap.add_argument("--copy-write", default="")
     ap.add_argument("--pmc-dirs", default="")
     ap.add_argument("--cu-count", type=int, default=256)
+    ap.add_argument("--attention", action="store_true",
+                    help="measure decode steps with the attention half instead of the metric's "
+                         "points")
+    ap.add_argument("--context", type=int, default=4096,
+                    help="tokens of each sequence, with --attention")
     args = ap.parse_args()
 
     if args.counters_summary:
@@ -732,6 +913,12 @@ def main():
         print("bench.py needs a GPU", file=sys.stderr)
         sys.exit(2)
     md.lib()  # fails loudly when the HIP library is missing
+    if args.attention:
+        rec = measure_attention(args)
+        print(json.dumps(rec), flush=True)
+        if not rec["valid"]:
+            sys.exit(1)
+        return
     names = [args.workload] if args.workload else POINTS
     extra = [] if args.workload or args.no_extra else EXTRA_POINTS
     ceiling = None

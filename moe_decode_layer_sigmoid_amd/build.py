@@ -16,8 +16,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_decode.so")
 SOURCES = ["api.hip", "router.hip", "experts_gemv.hip", "experts_mfma.hip", "epilogue.hip",
-           "experts_chain.hip", "probe.hip", "ops/ops_api.hip", "ops/quant.hip", "ops/product.hip",
-           "ops/cache_append.hip", "ops/cache_attend.hip", "ops/cache_evict.hip"]
+           "experts_chain.hip", "probe.hip"]
+# the operators beside the layer, in csrc/ops
+OPS_SOURCES = ["ops_api.hip", "quant.hip", "product.hip", "cache_append.hip", "cache_attend.hip",
+               "cache_evict.hip"]
 # experts_chain.hip is also compiled once per w13 chunk count (the first
 # template argument of its kernels), each into its own object, in parallel.
 CHAIN_NJG = range(1, 9)
@@ -52,10 +54,10 @@ def build(verbose: bool = False) -> str:
 
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
-    inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC, "-I", os.path.join(CSRC, "ops")]
+    inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
     jobs = []
-    for src in SOURCES:
-        obj = os.path.join(objdir, src.replace("/", "_").replace(".hip", ".o"))
+    for src in SOURCES + [os.path.join("ops", s) for s in OPS_SOURCES]:
+        obj = os.path.join(objdir, src.replace(os.sep, "_").replace(".hip", ".o"))
         jobs.append((obj, [hipcc(), *FLAGS, *inc, "-c", os.path.join(CSRC, src), "-o", obj]))
     for nj in CHAIN_NJG:
         obj = os.path.join(objdir, "experts_chain_njg%d.o" % nj)

@@ -86,13 +86,15 @@ __device__ __forceinline__ void tile_of(int id, int nt, int mt, int* n, int* m) 
 // instructions of their own and not the builtin, after which the compiler
 // waits for the load before the next read of any LDS, also of another buffer
 // (317 us instead of 271 at 8192 x 4096 x 6144): the kernel waits itself
-// before the barrier that hands a buffer over.
+// before the barrier that hands a buffer over.  m0, which they take the address
+// from, is reserved to the compiler and cannot be named as overwritten; it
+// sets m0 itself right before each instruction of its own that reads it.
 #define MOE_LOAD_TO_LDS(name, op)                                                           \
   __device__ __forceinline__ void name(const uint8_t* base, uint32_t off, uint32_t lds) {   \
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t" op " %1, %2"                             \
                  :                                                                          \
                  : "s"(lds), "v"(off), "s"(base)                                            \
-                 : "memory", "m0");                                                         \
+                 : "memory");                                                               \
   }
 MOE_LOAD_TO_LDS(load16_to_lds, "global_load_lds_dwordx4")
 MOE_LOAD_TO_LDS(load4_to_lds, "global_load_lds_dword")

@@ -354,9 +354,11 @@ class CachePlan(_PlanBase):
             mo = _rows(what, "mass_out", mass_out, _F32, (B, self._P), dev)
         if B == 0 or (T == 0 and not mo):
             return
-        rc = self._lib.moe_decode_cache_attend(
-            self._h, _pack_attend(*c, pq, sq, po, so, sm_scale, mi, mo), B, T,
-            _stream_of(stream, dev))
+        try:
+            a = _pack_attend(*c, pq, sq, po, so, sm_scale, mi, mo)
+        except OverflowError:
+            _need(False, what, "sm_scale must be finite in 32 bits")
+        rc = self._lib.moe_decode_cache_attend(self._h, a, B, T, _stream_of(stream, dev))
         if rc:
             _done(rc, what)
 
@@ -367,14 +369,18 @@ class CachePlan(_PlanBase):
         if not 0 <= B <= self._B:
             _need(False, what, "B must be in [0, %d]", self._B)
         table, row = (B, self._P), (B,)
-        a = _pack_evict(_rows(what, "page_table", page_table, _I32, table, dev),
-                        _rows(what, "seq_lens", seq_lens, _I32, row, dev),
-                        _rows(what, "mass", mass, _F32, table, dev),
-                        _rows(what, "out_table", out_table, _I32, table, dev),
-                        _rows(what, "out_lens", out_lens, _I32, row, dev),
-                        _rows(what, "out_mass", out_mass, _F32, table, dev),
-                        _rows(what, "freed", freed, _I32, table, dev),
-                        _rows(what, "n_freed", n_freed, _I32, row, dev), keep, sink, recent)
+        p = (_rows(what, "page_table", page_table, _I32, table, dev),
+             _rows(what, "seq_lens", seq_lens, _I32, row, dev),
+             _rows(what, "mass", mass, _F32, table, dev),
+             _rows(what, "out_table", out_table, _I32, table, dev),
+             _rows(what, "out_lens", out_lens, _I32, row, dev),
+             _rows(what, "out_mass", out_mass, _F32, table, dev),
+             _rows(what, "freed", freed, _I32, table, dev),
+             _rows(what, "n_freed", n_freed, _I32, row, dev))
+        try:
+            a = _pack_evict(*p, keep, sink, recent)
+        except struct.error:
+            _need(False, what, "keep, sink and recent must be integers of 32 bits")
         if B == 0:
             return
         rc = self._lib.moe_decode_cache_evict(self._h, a, B, _stream_of(stream, dev))
