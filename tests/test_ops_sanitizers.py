@@ -3,12 +3,22 @@ and UndefinedBehaviorSanitizer (ops_driver.c), as test_host_sanitizers does for
 the layer's.  No device is touched."""
 
 import os
+import subprocess
 from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 
 from moe_decode_layer_sigmoid_amd import build as lib_build
-from test_host_sanitizers import HERE, ROOT, SAN_ENV, _run
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HERE = os.path.join(ROOT, "tests", "sanitize")
+SAN_ENV = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:abort_on_error=0",
+               UBSAN_OPTIONS="print_stacktrace=1:halt_on_error=1")
+
+
+def _run(cmd, **kw):
+    res = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True, **kw)
+    return res.returncode, res.stdout
 
 
 def test_ops_host_checks_under_asan_ubsan(tmp_path):
