@@ -32,10 +32,10 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kRows = 16;
 constexpr int kTeams = kThreads / 16;  // sixteen threads that hold one row
 constexpr int kXcds = 8;
-// Workgroups of a launch: one per CU.  Measured at one sequence of 131000
-// tokens, 8 kv heads of 128, in an earlier form of this kernel: 50.6 us; two
-// per CU 57.5 (the same bytes from twice as many places at once, and twice the
-// parts to join), one of 512 threads 52.7.
+// Workgroups of a launch: one per CU.  Measured with one, one and a half, two
+// per CU (the same bytes from more places at once, and more parts to join): one
+// sequence of 131000 tokens, 8 kv heads of 128, 48.9, 57.8, 53.8 us; 8 of 16000,
+// 8 kv heads of 64, 13.8, 14.3, 13.7 us; of 256, 33.0, 44.3, 42.0 us.
 constexpr int kWantGroups = 256;
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
@@ -88,7 +88,8 @@ __device__ __forceinline__ float groups_sum(float v) {
   return v + __shfl_xor(v, 32, kWave);
 }
 
-// Least pages of a worker's share: one for each wave.
+// Least share of a worker: a page for each wave.  Measured with 4, 8, 16: one
+// sequence of 1000 tokens 9.3, 10.4, 10.3 us, of 4000 10.8, 11.4, 13.2 us.
 constexpr int kMinChunk = kWaves;
 
 // What a sequence costs a worker beside its pages, in pages: its waves joined,

@@ -162,7 +162,9 @@ int moe_decode_quant(const void* x, int64_t x_stride, int32_t M, int32_t K, floa
   const int64_t cols = limit > 0.f ? 2 * static_cast<int64_t>(K) : K;
   if (!aligned(x, 16) || !aligned(codes, 8) || x_stride < cols || x_stride % 8)
     return MOE_DECODE_ERR_INVALID_ARG;
-  if (K % moe::kBlock || K > kMaxK || M > kMaxRows || x_stride > (int64_t{1} << 31))
+  // a launch has fewer than 2^32 threads, one for eight values (and room)
+  if (K % moe::kBlock || K > kMaxK || M > kMaxRows || x_stride > (int64_t{1} << 31) ||
+      static_cast<int64_t>(M) * K > int64_t{1} << 34)
     return MOE_DECODE_ERR_UNSUPPORTED;
   if (M == 0) return MOE_DECODE_OK;
   return status(moe::launch_quant(static_cast<const uint16_t*>(x), x_stride, M, K, limit,

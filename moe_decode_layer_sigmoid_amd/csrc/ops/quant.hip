@@ -135,7 +135,6 @@ __global__ __launch_bounds__(kThreads) void quant_kernel(const uint16_t* __restr
 hipError_t launch_quant(const uint16_t* x, int64_t x_stride, int M, int K, float limit,
                         uint8_t* codes, uint8_t* scales, hipStream_t s) {
   const int64_t blocks = static_cast<int64_t>(M) * (K / kBlock);
-  if (blocks > INT32_MAX) return hipErrorInvalidValue;  // codes alone of 256 GiB
   const unsigned grid = static_cast<unsigned>((blocks + kThreads / 16 - 1) / (kThreads / 16));
   if (limit > 0.f)
     hipLaunchKernelGGL(quant_kernel<true>, dim3(grid), dim3(kThreads), 0, s, x, x_stride,

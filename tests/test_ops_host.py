@@ -17,7 +17,8 @@ P = 0x10000  # stands for an aligned device pointer; checks do not dereference
 
 @pytest.mark.parametrize("kw,code", [
     (dict(x=None), BAD), (dict(codes=None), BAD), (dict(scales=None), BAD), (dict(M=-1), BAD),
-    (dict(K=0), BAD), (dict(limit=-1.0), BAD), (dict(limit=math.nan), BAD), (dict(limit=1e19, stride=512), BAD), (dict(x=P + 8), BAD),
+    (dict(K=0), BAD), (dict(limit=-1.0), BAD), (dict(limit=math.nan), BAD), (dict(limit=1e19, stride=512), BAD),
+    (dict(M=(1 << 20) - 1, K=16512, stride=16512), UNS), (dict(M=(1 << 18) + 1, K=65536, stride=65536), UNS), (dict(x=P + 8), BAD),
     (dict(codes=P + 4), BAD), (dict(stride=255), BAD), (dict(stride=260), BAD),
     (dict(limit=7.0, stride=264), BAD), (dict(K=100, stride=256), UNS),
     (dict(K=65664, stride=65664), UNS), (dict(M=(1 << 20) + 1), UNS), (dict(M=0), OK),
