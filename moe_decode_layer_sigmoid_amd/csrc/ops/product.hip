@@ -483,6 +483,146 @@ hipError_t launch_rows(const ProductArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// fp32 outputs of many rows and columns: a 64 x 64 tile per workgroup, its
+// columns' blocks dealt out over eight waves, each of which takes the whole tile.
+// So a code is converted once for four matrix instructions (two in the tile
+// kernel's waves of 32 x 32, where conversions set the time), and no wave waits
+// for another before the end.  A wave's block goes to its own LDS area, from
+// there to registers, and the next block is on its way while this one is
+// multiplied.  The waves' sums are added in LDS, in order.  Bound by the wave's
+// own sequence of LDS reads, conversions and products, about 2.3 us a block of
+// eight waves.  Measured against the tile kernel: 333 x 5003 x 6144 35 us (40),
+// 64 x 16000 x 6144 27.9 (33.9), 128 x 8000 x 4096 15.7 (19.8); where its tiles
+// leave a last round of CUs empty, the tile kernel stays (600 x 4096 x 4096 36.3,
+// this one 39.5; 4096 x 4096 x 4096 111, 203).
+constexpr int kDealWaves = 8, kDealTile = 64;
+
+template <bool E8>
+__global__ __launch_bounds__(64 * kDealWaves) void product_deal_kernel(ProductArgs a) {
+  constexpr int T = kDealTile / 16;
+  constexpr int kArea = 2 * kDealTile * kBlock;  // bytes of a wave's block, and of its sums
+  constexpr int kLoads = kArea / 1024;
+  static_assert(kArea == kDealTile * kDealTile * 4, "the sums take the areas");
+  __shared__ __attribute__((aligned(16))) unsigned char smem[kDealWaves * kArea];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  int tn, tm;
+  tile_of(blockIdx.x, (a.N + kDealTile - 1) / kDealTile, (a.M + kDealTile - 1) / kDealTile, &tn,
+          &tm);
+  const int n0 = tn * kDealTile, m0 = tm * kDealTile;
+  const int KB = a.K / kBlock;
+  const uint8_t* wbase = a.w + static_cast<size_t>(n0) * a.K;
+  const uint8_t* xbase = a.x + static_cast<size_t>(m0) * a.K;
+  const uint8_t* sbase = a.xs + static_cast<size_t>(m0) * KB;
+  const size_t ws0 = static_cast<size_t>(n0 / kBlock) * KB;
+  unsigned char* area = smem + wave * kArea;
+  const uint32_t lds0 = lds_address(area);
+  // load j: rows 8 j .. 8 j + 7, weight rows first, swizzled as in the tile kernel
+  uint32_t src[kLoads], soff[T];
+#pragma unroll
+  for (int j = 0; j < kLoads; ++j) {
+    const int r = 8 * j + (lane >> 3), piece = (lane & 7) ^ ((r >> 1) & 7);
+    const int row = j < kLoads / 2 ? min(r, a.N - 1 - n0) : min(r - kDealTile, a.M - 1 - m0);
+    src[j] = static_cast<uint32_t>(row) * static_cast<uint32_t>(a.K) + 16 * piece;
+  }
+#pragma unroll
+  for (int t = 0; t < T; ++t)
+    soff[t] = static_cast<uint32_t>(min(16 * t + c, a.M - 1 - m0)) * KB;
+  const int o0 = 128 * c + 16 * ((2 * g) ^ (c >> 1)), o1 = 128 * c + 16 * ((2 * g + 1) ^ (c >> 1));
+  f32x4_t acc[T][T];
+#pragma unroll
+  for (int i = 0; i < T; ++i)
+#pragma unroll
+    for (int t = 0; t < T; ++t) acc[i][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  int sx[T];
+  uint32_t sw = 0;
+  auto load_block = [&](int kb) {
+#pragma unroll
+    for (int t = 0; t < T; ++t) sx[t] = sbase[soff[t] + kb];
+    sw = E8 ? static_cast<const uint8_t*>(a.ws)[ws0 + kb]
+            : static_cast<const uint32_t*>(a.ws)[ws0 + kb];
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+      load16_to_lds((j < kLoads / 2 ? wbase : xbase) + kb * kBlock, src[j], lds0 + 1024 * j);
+  };
+  load_block(wave);  // K has a block for every wave
+  for (int kb = wave; kb < KB; kb += kDealWaves) {
+    wait_loads<0>();
+    float s[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+      s[t] = (E8 ? e8m0_to_f32(sw) : __uint_as_float(sw)) * e8m0_to_f32(sx[t]);
+    uint4 w[T][2];
+    bf16x8_t xq[T][4];
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const unsigned char* p = area + (T + t) * 2048;
+      const uint4 x0 = *reinterpret_cast<const uint4*>(p + o0);
+      const uint4 x1 = *reinterpret_cast<const uint4*>(p + o1);
+      xq[t][0] = codes_bf16(x0.x, x0.y);
+      xq[t][1] = codes_bf16(x0.z, x0.w);
+      xq[t][2] = codes_bf16(x1.x, x1.y);
+      xq[t][3] = codes_bf16(x1.z, x1.w);
+    }
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      w[i][0] = *reinterpret_cast<const uint4*>(area + i * 2048 + o0);
+      w[i][1] = *reinterpret_cast<const uint4*>(area + i * 2048 + o1);
+    }
+    // every read of the area is done before the next block goes there
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    // past the end: this block again, so that no branch stands around the loads
+    load_block(kb + kDealWaves < KB ? kb + kDealWaves : kb);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      bf16x8_t wq[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        wq[2 * h] = codes_bf16(w[i][h].x, w[i][h].y);
+        wq[2 * h + 1] = codes_bf16(w[i][h].z, w[i][h].w);
+      }
+      f32x4_t d[T];
+#pragma unroll
+      for (int t = 0; t < T; ++t) d[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+          d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wq[q], xq[t][q], d[t], 0, 0, 0);
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][t][e] = fmaf(s[t], d[t][e], acc[i][t][e]);
+    }
+  }
+  wait_loads<0>();  // the last loads, before the area takes the sums
+  f32x4_t* mine = reinterpret_cast<f32x4_t*>(area) + lane;
+#pragma unroll
+  for (int i = 0; i < T; ++i)
+#pragma unroll
+    for (int t = 0; t < T; ++t) mine[(i * T + t) * 64] = acc[i][t];
+  __syncthreads();
+  const f32x4_t* sums = reinterpret_cast<const f32x4_t*>(smem) + lane;
+  constexpr int kEach = T * T / kDealWaves;  // 16 x 16 tiles of a wave
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    const int p = wave * kEach + j, i = p / T, t = p % T;
+    f32x4_t v = sums[p * 64];
+    for (int k = 1; k < kDealWaves; ++k) v += sums[(k * T * T + p) * 64];
+    store4<true>(a, m0 + 16 * t + c, n0 + 16 * i + 4 * g, v);
+  }
+}
+
+hipError_t launch_deal(const ProductArgs& a, hipStream_t s) {
+  const unsigned tiles = static_cast<unsigned>((a.N + kDealTile - 1) / kDealTile) *
+                         ((a.M + kDealTile - 1) / kDealTile);
+  hipLaunchKernelGGL(a.e8m0 ? product_deal_kernel<true> : product_deal_kernel<false>, dim3(tiles),
+                     dim3(64 * kDealWaves), 0, s, a);
+  return hipGetLastError();
+}
+
 // The shapes, and what a round of one costs in 10 ns, alone on its CU and per
 // workgroup of a CU that has several (measured at K = 6144 and 1024, N = 128
 // to 8192, 1 to 4096 rows, codes past the Infinity Cache).
@@ -500,6 +640,8 @@ constexpr Shape kShapes[] = {{Tile64x32::TN, Tile64x32::TM, 36, 20, 41, 26},
                              {Tile128::TN, Tile128::TM, 80, 80, 116, 116},
                              {Tile256::TN, Tile256::TM, 208, 208, 360, 360}};
 constexpr int kRowsShape = 4;  // product_rows_kernel
+constexpr int kDealShape = 5;  // product_deal_kernel
+constexpr int kDealStep = 240, kDealFixed = 340;  // of it, in 10 ns
 constexpr int kCus = 256;
 // Splits only where all parts run at once: at most two workgroups per CU.
 constexpr int kMaxParts = 2 * kCus;
@@ -538,6 +680,16 @@ Choice choose(int M, int N, int K, bool f32) {
         best = {i, splits, static_cast<size_t>(tiles)};
       }
     }
+  }
+  if (f32 && M > 32 && KB >= kDealWaves) {
+    // the dealing kernel: rounds of one workgroup per CU, each some setting up
+    // and joining and a step for every eight blocks (up to 32 rows waste half its
+    // tile: 20 x 16000 x 4096 15.8 us, else 14.1)
+    const int64_t tiles = static_cast<int64_t>((N + kDealTile - 1) / kDealTile) *
+                          ((M + kDealTile - 1) / kDealTile);
+    const int64_t cost = (tiles + kCus - 1) / kCus *
+                         ((KB + kDealWaves - 1) / kDealWaves * kDealStep + kDealFixed);
+    if (cost < least) best = {kDealShape, 1, static_cast<size_t>(tiles)};
   }
   return best;
 }
@@ -592,6 +744,7 @@ hipError_t launch_product(const ProductArgs& a0, void* ws, size_t ws_bytes, hipS
   a.part = reinterpret_cast<float*>(a.count + kMaxParts);
   switch (c.shape) {
     case kRowsShape: return launch_rows(a, s);
+    case kDealShape: return launch_deal(a, s);
     case 0: return a.splits > 1 ? launch_tile<Tile64x32, true>(a, s) : launch_tile<Tile64x32, false>(a, s);
     case 1: return a.splits > 1 ? launch_tile<Tile64, true>(a, s) : launch_tile<Tile64, false>(a, s);
     case 2: return launch_tile<Tile128, false>(a, s);

@@ -151,6 +151,23 @@ def test_product(M, N, K, fmt):
         plan.close()
 
 
+@pytest.mark.parametrize("fmt", ["fp32", "e8m0"])
+@pytest.mark.parametrize("M,N,K", [(40, 16000, 2048), (65, 8100, 4096), (100, 4900, 6272), (333, 5003, 6144)])
+def test_product_fp32_outputs_of_many_columns(M, N, K, fmt):
+    """Columns dealt out over waves, in even and uneven shares."""
+    codes, scales, w, ws = product_inputs(M * K, M, N, K, fmt)
+    plan = md.ProductPlan(md.make_product_desc(N, K, M, fmt, "fp32"))
+    wide = torch.full((M + 2, N + 3), 7.0, device="cuda")
+    args = dict(codes=codes.cuda(), scales=scales.cuda(), w=w.cuda(), w_scale=ws.cuda())
+    plan.run(M, out=wide[1:M + 1, 1:N + 1], **args)
+    check_product(codes, scales, w, ws, wide[1:M + 1, 1:N + 1], 2.0 ** -24)
+    assert (wide[0] == 7).all() and (wide[-1] == 7).all() and (wide[:, 0] == 7).all() and (wide[:, N + 1:] == 7).all()
+    again = torch.empty(M, N, device="cuda")
+    plan.run(M, out=again, **args)
+    assert again.equal(wide[1:M + 1, 1:N + 1])
+    plan.close()
+
+
 def test_product_fewer_rows_and_repeats():
     """A plan serves every row count up to its limit; the same call gives the
     same bits."""
