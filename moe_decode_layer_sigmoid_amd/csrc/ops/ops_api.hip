@@ -102,7 +102,7 @@ size_t cache_layout(const moe_decode_cache_desc& d, char* base, moe::AttendArgs*
   char* rec = take(mass * B * d.max_pages * heads * rows * 4);
   const size_t y = heads * (rows / 16);
   const size_t workers = moe::attend_workers(d.kv_heads, static_cast<int>(rows), d.max_batch,
-                                             d.max_pages);
+                                             d.max_pages, d.head_dim);
   char* part_o = take(y * (workers + B) * 16 * d.head_dim * 4);
   char* part_ml = take(y * (workers + B) * 16 * 2 * 4);
   char* count = take(y * B * 4);

@@ -88,7 +88,7 @@ struct AttendArgs {
   uint32_t* count;  // [y][B] parts handed in; 0 between runs
 };
 // Workgroups per kv head and row tile.
-int attend_workers(int Hkv, int max_rows, int max_batch, int max_pages);
+int attend_workers(int Hkv, int max_rows, int max_batch, int max_pages, int D);
 hipError_t launch_attend(const AttendArgs& a, hipStream_t s);
 
 struct EvictArgs {
