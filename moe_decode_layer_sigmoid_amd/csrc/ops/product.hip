@@ -85,7 +85,8 @@ __device__ __forceinline__ void tile_of(int id, int nt, int mt, int* n, int* m) 
 // to lds + 16 lane, a byte (as a dword) or a dword to lds + 4 lane.  As
 // instructions of their own and not the builtin, after which the compiler
 // waits for the load before the next read of any LDS, also of another buffer
-// (317 us instead of 271 at 8192 x 4096 x 6144): the kernel waits itself
+// (317 us instead of 271 at 8192 x 4096 x 6144, when this was the only
+// difference; 196 with what came after): the kernel waits itself
 // before the barrier that hands a buffer over.  m0, which they take the address
 // from, is reserved to the compiler and cannot be named as overwritten; it
 // sets m0 itself right before each instruction of its own that reads it.

@@ -11,7 +11,9 @@
 // exponent, the block is computed again in 64 bits: about one block in 300.
 // Measured at 4096 x 2048 (42 MB): 12.2 us, 3.4 TB/s; everywhere in 64 bits
 // 20.0 us.  Bound by the vector unit (270 instructions a wave, 4 waves a row of
-// 2048) about as much as by the bytes (8.6 us at a copy's rate).
+// 2048) about as much as by the bytes (8.6 us at a copy's rate); two blocks a
+// thread, loaded together, 13.5 us, four 14.4.  Plain values, 4096 x 4096: 10.6
+// us, 4.8 TB/s, a copy's rate.
 #include "ops_device.h"
 #include "ops_launch.h"
 
